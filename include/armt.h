@@ -38,6 +38,8 @@
 #ifndef ARMT_H_
 #define ARMT_H_
 
+#include <stddef.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -336,6 +338,80 @@ armt_status armt_test_bounded_wait(void* stream);
 armt_status armt_memory_write_static(int M, int d, int d_key, int nu, float eps,
                                      const float* m, const float* wk, const float* wv,
                                      float* A, float* z, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The ends of the model: token embedding, the norm in front of the head, and
+ * the loss over the vocabulary, each with its gradients.  (The pages have no
+ * counterpart: they feed embeddings in and read hidden states out.)
+ *
+ * dtype is ARMT_FP32 or ARMT_BF16, one type for all tensors marked [type];
+ * sums, norms and softmax statistics are fp32 in both.  Tensors are dense and
+ * row-major, d a multiple of 8, their base addresses on 16-byte boundaries.
+ * ids / targets are int32 (id_bytes 4) or int64 (8).  All pointers are device
+ * pointers of the current device.  Everything is asynchronous on `stream`,
+ * allocates nothing and can be captured into a CUDA graph; calls that share a
+ * workspace must be ordered on one stream.  Results do not depend on the
+ * order in which the device runs the work (no floating-point atomics).
+ * Errors: INVALID_ARG (null or misaligned pointer, non-positive size, type,
+ * workspace too small, a scale that is not finite), UNSUPPORTED (d % 8, or d
+ * above 16384 in the norm), CUDA.
+ * ---------------------------------------------------------------------- */
+
+/* out[n, d] = scale * table[ids[n], :] ([type], table [vocab, d]); a row of
+ * zeros where the id is outside [0, vocab) (padding). */
+armt_status armt_embed(armt_dtype dtype, int n, int vocab, int d, const void* ids, int id_bytes, const void* table,
+                       float scale, void* out, void* stream);
+
+/* Gradient of the table: d_table[v, :] = scale * sum of d_out[n, :] over the n
+ * with ids[n] = v, in the order of n ([type], d_table [vocab, d]); with
+ * accumulate 1 the sum is added to what d_table holds (a table shared with
+ * the head) and rows that no id names are left as they are.  Ids outside
+ * [0, vocab) have no gradient.  The workspace may be null when its size is 0. */
+armt_status armt_embed_grad_workspace(armt_dtype dtype, int n, int vocab, int d, size_t* bytes);
+armt_status armt_embed_grad(armt_dtype dtype, int n, int vocab, int d, const void* ids, int id_bytes,
+                            const void* d_out, float scale, void* d_table, int accumulate, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* y = x * rstd * gain per row, rstd = (mean x^2 + eps)^-1/2 ([type] x, y
+ * [n, d], gain [d]; rstd [n] fp32, optional).  y may be x. */
+armt_status armt_rms_norm(armt_dtype dtype, int n, int d, const void* x, const void* gain, float eps, void* y,
+                          float* rstd, void* stream);
+
+/* Gradients of armt_rms_norm from its x and rstd and the gradient dy of its
+ * result: dx [n, d] and d_gain [d] ([type]).  dx may be dy or x. */
+armt_status armt_rms_norm_grad_workspace(armt_dtype dtype, int n, int d, size_t* bytes);
+armt_status armt_rms_norm_grad(armt_dtype dtype, int n, int d, const void* x, const void* gain, const float* rstd,
+                               const void* dy, void* dx, void* d_gain, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* Softmax cross entropy of hidden [n, d] against head [vocab, d] ([type]):
+ * with l = scale * hidden head^T, lse[i] = log sum exp l[i, :] and loss[i] =
+ * lse[i] - l[i, targets[i]] ([n] fp32).  Rows whose target is outside
+ * [0, vocab) are skipped: loss and lse are 0 there, whatever the row holds.
+ * The logits are never kept: the workspace holds two numbers per row and 128
+ * vocabulary entries for 8192 rows at a time.
+ * _workspace: grad 0 for armt_token_loss, 1 for armt_token_loss_grad. */
+armt_status armt_token_loss_workspace(armt_dtype dtype, int n, int vocab, int d, int grad, size_t* bytes);
+armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d, const void* hidden, const void* head,
+                            const void* targets, int target_bytes, float scale, float* loss, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum_i d_loss[i] * loss[i] (d_loss [n] fp32) to hidden and head
+ * ([type]; either may be null), from the lse of armt_token_loss with the same
+ * inputs.  The logits are computed again, one piece of the vocabulary at a
+ * time; softmax minus one-hot, divided by the largest |d_loss|, enters the
+ * products as bf16 (as three bf16 terms, 24 bits, for fp32).  Rows without a
+ * target have a zero gradient and add nothing to the head's, whatever they
+ * hold (d_loss and lse of such rows are not read). */
+armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, int d, const void* hidden, const void* head,
+                                 const void* targets, int target_bytes, float scale, const float* lse,
+                                 const float* d_loss, void* d_hidden, void* d_head, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Wait for `stream`, then report whether a bounded wait ran out in the last
+ * armt_token_loss or armt_token_loss_grad call that used this workspace
+ * (ARMT_ERR_DEVICE_TIMEOUT; its results are NaN then), ARMT_OK otherwise. */
+armt_status armt_workspace_status(const void* workspace, void* stream);
 
 #ifdef __cplusplus
 }

@@ -35,6 +35,9 @@ EXPORTS = (
     "armt_status_string", "armt_last_error", "armt_grouped_gemm", "armt_memory_write",
     "armt_kernel_kinds", "armt_kernel_kind_name", "armt_profile_forward", "armt_memory_write_static",
     "armt_forward_ex", "armt_test_bounded_wait", "armt_stage_wave",
+    "armt_embed", "armt_embed_grad", "armt_embed_grad_workspace", "armt_rms_norm", "armt_rms_norm_grad",
+    "armt_rms_norm_grad_workspace", "armt_token_loss", "armt_token_loss_grad", "armt_token_loss_workspace",
+    "armt_workspace_status",
 )
 
 
@@ -100,6 +103,17 @@ def lib() -> ctypes.CDLL:
     L.armt_kernel_kind_name.restype = ctypes.c_char_p
     L.armt_profile_forward.argtypes = [vp, vp, c_int, c_int, vp, vp, vp, vp,
                                        ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_int)]
+    c_size, p_size = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+    L.armt_embed.argtypes = [c_int] * 4 + [vp, c_int, vp, c_float, vp, vp]
+    L.armt_embed_grad_workspace.argtypes = [c_int] * 4 + [p_size]
+    L.armt_embed_grad.argtypes = [c_int] * 4 + [vp, c_int, vp, c_float, vp, c_int, vp, c_size, vp]
+    L.armt_rms_norm.argtypes = [c_int] * 3 + [vp, vp, c_float, vp, vp, vp]
+    L.armt_rms_norm_grad_workspace.argtypes = [c_int] * 3 + [p_size]
+    L.armt_rms_norm_grad.argtypes = [c_int] * 3 + [vp] * 7 + [c_size, vp]
+    L.armt_token_loss_workspace.argtypes = [c_int] * 5 + [p_size]
+    L.armt_token_loss.argtypes = [c_int] * 4 + [vp, vp, vp, c_int, c_float, vp, vp, vp, c_size, vp]
+    L.armt_token_loss_grad.argtypes = [c_int] * 4 + [vp, vp, vp, c_int, c_float] + [vp] * 5 + [c_size, vp]
+    L.armt_workspace_status.argtypes = [vp, vp]
     for name in EXPORTS:
         if name not in ("armt_status_string", "armt_last_error", "armt_kernel_kind_name"):
             getattr(L, name).restype = c_int
@@ -224,6 +238,35 @@ class Armt:
         _check(L.armt_profile_forward(self._h, _ptr(emb), n_segments, seg_len, _ptr(out_hidden), _ptr(out_A),
                                       _ptr(out_z), _stream_handle(stream), ms, cnt), "armt_profile_forward", self._h)
         return {L.armt_kernel_kind_name(k).decode(): (ms[k], cnt[k]) for k in range(n) if cnt[k]}
+
+    def score(self, ids, targets, n_segments: int, seg_len: int, table, head, gain, loss, A, z,
+              embed_scale: float = 1.0, logit_scale: float = 1.0, carry_state: bool = False, stream=None):
+        """Per-token losses of a token sequence: embedding, forward, the norm in front
+        of the head (gain; None leaves it out) and the vocabulary loss.
+
+        ids, targets [n_segments * seg_len] (an id outside the table is padding, a
+        target outside the vocabulary has loss 0); table, head [vocab, d] and gain [d]
+        in the context's type; loss [n_segments * seg_len] fp32; A, z as in
+        ``forward_ex``.  The embeddings, hidden states and workspaces live for the
+        call, in PyTorch's allocator, on the call's stream."""
+        from . import operators as ops
+        n, d = n_segments * seg_len, self.cfg.d_model
+        for name, t in (("ids", ids), ("targets", targets)):
+            if t.numel() != n:
+                raise ArmtError(1, "Armt.score", f"{name} must hold n_segments * seg_len ids")
+        if table.shape[-1] != d or head.shape[-1] != d:
+            raise ArmtError(1, "Armt.score", "table and head must be as wide as the model")
+        if table.dtype != ops.torch_type(self.cfg.dtype):
+            raise ArmtError(1, "Armt.score", "table, head and gain must have the context's type")
+        with ops.on_stream(stream, table.device):
+            x = table.new_empty(n, d)
+            ops.embed(ids, table, x, scale=embed_scale)
+            hidden = table.new_empty(n, d)
+            self.forward_ex(x, n_segments, seg_len, hidden, A, z, carry_state)
+            if gain is not None:
+                ops.rms_norm(hidden, gain, hidden, None, self.cfg.rms_eps)
+            lse = loss.new_empty(n)
+            ops.token_loss(hidden, head, targets, loss, lse, scale=logit_scale)
 
     def device_status(self, stream=None):
         _check(lib().armt_device_status(self._h, _stream_handle(stream)), "armt_device_status", self._h)

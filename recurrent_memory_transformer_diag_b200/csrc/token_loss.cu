@@ -1,0 +1,1038 @@
+// Softmax cross entropy over a large vocabulary, straight from hidden states
+// and head weights, with its gradients; the logits are never kept.
+//
+//   l[n][v] = scale * h_n . w_v        lse_n = log sum_v exp l[n][v]
+//   loss_n  = lse_n - l[n][t_n]        (0 for a row without a target)
+//   P[n][v] = g_n (exp(l[n][v] - lse_n) - [v = t_n])
+//   dH = scale P W       dW = scale P^T H
+//
+// One tensor-core kernel computes every product, in three roles:
+//   LSE   logits tile by tile; each tile leaves (max, sum of exponentials) of
+//         its columns per row and the target's logit, joined by a small kernel
+//   PROB  logits of one vocabulary piece again, turned into P (bf16)
+//   GRAD  both gradients of the piece from P in one launch: dW tiles contract
+//         over the rows, dH tiles over the piece's columns
+// A piece of the vocabulary is as wide as P of that piece stays within a fixed
+// budget, so the memory is independent of the vocabulary.
+//
+// Rows are put in order first: rows with a target in front, the others behind
+// them as zeros (so what stands in a masked row cannot reach the head's
+// gradient), and the products stop at the last row with a target.
+//
+// Accumulation: tcgen05 adds into fp32 accumulators with truncation, measured
+// here as a relative error of about 2e-6 at K = 2048 growing with K.  Where
+// the result is read in fp32 (the logits; everything of fp32 operands) the
+// accumulator therefore covers `chunk` k-blocks only and the epilogue threads
+// add the chunks in registers, rounded to nearest.
+//
+// fp32 operands: x = hi + mid + lo with three bf16 terms (24 bits), and the six
+// products hi lo, lo hi, mid mid, hi mid, mid hi, hi hi run one after another
+// into the same sums; the dropped ones are below 2^-24 of the result.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cmath>
+#include <mutex>
+
+#include "armt_internal.cuh"
+#include "tcgen05_ptx.cuh"
+#include "vec8.cuh"
+
+namespace armt {
+
+namespace {
+
+using namespace tc;
+
+constexpr int TILE = 256;              // rows and columns of a CTA pair's tile (each CTA: 128 rows)
+constexpr int BK = 64;                 // 64 bf16 = 128 bytes = one swizzle row
+constexpr int STAGES = 6;
+constexpr int BOX_BYTES = 64 * BK * 2; // one copied box: 64 x 64 bf16
+constexpr int STAGE_BYTES = 4 * BOX_BYTES;   // two boxes of A, two of B
+constexpr int EPI_WARPS = 8;
+constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
+constexpr int SLOT_BYTES = 4096;       // per epilogue warp: 32 rows x 128 bytes of output
+constexpr int SLOT_OFFSET = STAGES * STAGE_BYTES;
+constexpr int BAR_OFFSET = SLOT_OFFSET + EPI_WARPS * SLOT_BYTES;
+constexpr int SMEM_TOTAL = BAR_OFFSET + 256 + 1024;   // + alignment slack
+static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory per CTA");
+
+constexpr int ROW_GROUP = 32;          // row tiles that share a vocabulary tile before the next one
+constexpr int LOGIT_CHUNK = 4;         // k-blocks per accumulator where the sum is read in fp32
+constexpr float LOG2E = 1.4426950408889634f;
+
+enum Role { LSE = 0, PROB = 1, GRAD = 2 };
+
+struct LossParams {
+  int n_rows, d, vocab;
+  int planes;                 // 1: bf16 operands; 3: fp32 operands as three bf16 terms
+  int v0, vc;                 // vocabulary piece
+  int chunk;                  // k-blocks per accumulator
+  float scale;
+  const int* n_valid;         // rows with a target (device)
+  const int* target;          // per row in order
+  // LSE
+  float2* part; int part_pitch; float* target_logit;
+  // PROB
+  const float* lse; const float* g;
+  // GRAD
+  int want_dw, want_dh, splits, k_split, dh_add, dw_bf16;
+  const float* g_max;
+  unsigned* err;
+};
+
+struct LossMaps {
+  CUtensorMap a, b, c;        // operands: LSE/PROB hidden, head; GRAD P, head, hidden
+  CUtensorMap out0, out1;     // PROB: P; GRAD: dW, dH partial sums
+};
+
+// Terms multiplied in product q of fp32 operands (smallest products first).
+__device__ __forceinline__ int term_a(int q) { return (0x021010 >> (4 * (5 - q))) & 15; }
+__device__ __forceinline__ int term_b(int q) { return (0x201100 >> (4 * (5 - q))) & 15; }
+
+// One tile of work: D[256 x 256] = A B^T over k-blocks kb = 0 .. kblocks-1.
+struct Job {
+  int m0, n0;        // first row / column in the operands' own coordinates
+  int ka, kb;        // first k coordinate in A / B
+  int kblocks;
+  bool dw;           // GRAD: a tile of dW (A is P transposed)
+  int split;         // GRAD, dH: which partial sum
+  int ntile;         // LSE: index of the vocabulary tile
+};
+
+template <int ROLE>
+struct Jobs {
+  int mt, nt, dt, total, n_dw;
+  __device__ Jobs(const LossParams& p, int nv) {
+    mt = (nv + TILE - 1) / TILE;
+    nt = (p.vc + TILE - 1) / TILE;
+    dt = (p.d + TILE - 1) / TILE;
+    if (ROLE == GRAD) {
+      n_dw = p.want_dw ? nt * dt : 0;
+      total = n_dw + (p.want_dh ? mt * dt * p.splits : 0);
+    } else {
+      n_dw = 0;
+      total = mt * nt;
+    }
+  }
+  __device__ Job get(const LossParams& p, int nv, int t) const {
+    Job j;
+    j.dw = false;
+    j.split = 0;
+    j.ntile = 0;
+    if (ROLE != GRAD) {
+      // consecutive tiles share a vocabulary tile: the head is read from HBM
+      // once per group of rows, the group's hidden rows stay in L2
+      const int per = ROW_GROUP * nt;
+      const int grp = t / per, r = t - grp * per;
+      const int mg = min(ROW_GROUP, mt - grp * ROW_GROUP);
+      j.ntile = r / mg;
+      j.m0 = (grp * ROW_GROUP + r - j.ntile * mg) * TILE;
+      j.n0 = p.v0 + j.ntile * TILE;
+      j.ka = j.kb = 0;
+      j.kblocks = (p.d + BK - 1) / BK;
+    } else if (t < n_dw) {
+      j.dw = true;
+      j.m0 = (t / dt) * TILE;
+      j.n0 = (t % dt) * TILE;
+      j.ka = j.kb = 0;
+      j.kblocks = (nv + BK - 1) / BK;
+    } else {
+      int r = t - n_dw;
+      j.n0 = (r % dt) * TILE;
+      r /= dt;
+      j.m0 = (r % mt) * TILE;
+      j.split = r / mt;
+      j.ka = j.split * p.k_split;
+      j.kb = p.v0 + j.ka;
+      j.kblocks = (min(p.vc - j.ka, p.k_split) + BK - 1) / BK;
+    }
+    return j;
+  }
+};
+
+// Shared-memory operand descriptors (128-byte swizzle).  A box is 64 rows of
+// 128 bytes.  K-major: the rows are the tile's rows, 8-row groups 1024 bytes
+// apart, 32 bytes per K = 16.  MN-major (the operand stored with k as rows):
+// a row holds 64 of the tile's rows, the next 64 are the next box (leading
+// offset), 8-k groups 1024 bytes apart, 2048 bytes per K = 16.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, bool mn) {
+  uint64_t d = sw128_desc(saddr);
+  if (mn) d += (uint64_t)((BOX_BYTES >> 4) - 1) << 16;   // LBO 1 -> one box
+  return d;
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
+// The slot of this warp may be written again (its last store has been read).
+__device__ __forceinline__ void slot_free(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+
+// 16-byte piece q of this lane's row in the slot (128-byte swizzle).
+__device__ __forceinline__ uint4* slot_piece(uint8_t* slot, int lane, int q) {
+  return reinterpret_cast<uint4*>(slot + lane * 128 + ((q ^ (lane & 7)) << 4));
+}
+
+__device__ __forceinline__ void slot_store(const CUtensorMap* map, uint8_t* slot, int lane, int c0, int c1, int c2,
+                                           bool add) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (add) tma_add_3d(map, slot, c0, c1, c2);
+    else tma_store_3d(map, slot, c0, c1, c2);
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+
+// 64 values per lane (a row each) as bf16: columns c0 .. c0+63 of rows c1 .. c1+31.
+__device__ __forceinline__ void emit_bf16x64(const CUtensorMap* map, uint8_t* slot, int lane, const float* v, int c0,
+                                             int c1, int c2) {
+  slot_free(lane);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    uint4 pk;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&pk);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[q * 8 + 2 * i], v[q * 8 + 2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b2);
+    }
+    *slot_piece(slot, lane, q) = pk;
+  }
+  slot_store(map, slot, lane, c0, c1, c2, false);
+}
+
+__device__ __forceinline__ void emit_f32x32(const CUtensorMap* map, uint8_t* slot, int lane, const float* v, int c0,
+                                            int c1, int c2, bool add) {
+  slot_free(lane);
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    *slot_piece(slot, lane, q) = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                            __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+  slot_store(map, slot, lane, c0, c1, c2, add);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Epilogue of one tile: acc holds this thread's row (TMEM lane) of 128
+// columns, those of its half of the tile.
+template <int ROLE>
+__device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps& maps, const Job& j, int nv,
+                                            float (&acc)[128], int row_in_tile, int half, int lane, uint8_t* slot) {
+  const int row = j.m0 + row_in_tile;
+  const int wrow0 = row - lane;
+  const int col0 = j.n0 + half * 128;
+  if constexpr (ROLE == LSE) {
+#pragma unroll
+    for (int i = 0; i < 128; ++i) acc[i] *= p.scale;
+    if (col0 + 128 > p.vocab) {   // the last tile: columns past the vocabulary do not count
+#pragma unroll
+      for (int i = 0; i < 128; ++i)
+        if (col0 + i >= p.vocab) acc[i] = -INFINITY;
+    }
+    float m = acc[0];
+#pragma unroll
+    for (int i = 1; i < 128; ++i) m = fmaxf(m, acc[i]);
+    const float ms = m == -INFINITY ? 0.f : m;
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+    for (int i = 0; i < 128; i += 4) {
+      s0 += ex2((acc[i] - ms) * LOG2E);
+      s1 += ex2((acc[i + 1] - ms) * LOG2E);
+      s2 += ex2((acc[i + 2] - ms) * LOG2E);
+      s3 += ex2((acc[i + 3] - ms) * LOG2E);
+    }
+    if (row < nv) {
+      p.part[(long long)(2 * j.ntile + half) * p.part_pitch + row] = make_float2(m, (s0 + s1) + (s2 + s3));
+      const unsigned at = (unsigned)(p.target[row] - col0);
+      if (at < 128u) {
+        float t = acc[0];
+#pragma unroll
+        for (int i = 1; i < 128; ++i)
+          if ((unsigned)i == at) t = acc[i];
+        p.target_logit[row] = t;
+      }
+    }
+  } else if constexpr (ROLE == PROB) {
+    const bool in = row < nv;
+    const float g = in ? p.g[row] : 0.f;
+    const float lse = in ? p.lse[row] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 128; ++i) acc[i] = g * ex2((acc[i] * p.scale - lse) * LOG2E);
+    if (in) {
+      const unsigned at = (unsigned)(p.target[row] - col0);
+      if (at < 128u) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i)
+          if ((unsigned)i == at) acc[i] -= g;
+      }
+    }
+    if (g == 0.f) {   // rows without a target or weight: zero whatever their logits are
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+    }
+    const int pc = col0 - p.v0;   // column in the piece
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (wrow0 >= p.n_rows || pc + 64 * h >= p.vc) continue;   // nothing of this box is in P
+      for (int t = 0; t < p.planes; ++t) {
+        emit_bf16x64(&maps.out0, slot, lane, acc + 64 * h, pc + 64 * h, wrow0, t);
+        if (t + 1 < p.planes) {   // what the term just written leaves of the value
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            const float r = acc[64 * h + i] - __bfloat162float(__float2bfloat16_rn(acc[64 * h + i]));
+            acc[64 * h + i] = r;
+          }
+        }
+      }
+    }
+  } else {
+    if (j.dw) {
+      if (wrow0 >= p.vc) return;
+      const float f = *p.g_max * p.scale;
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] *= f;
+      if (p.dw_bf16) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (col0 + 64 * h < p.d) emit_bf16x64(&maps.out0, slot, lane, acc + 64 * h, col0 + 64 * h, p.v0 + wrow0, 0);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          if (col0 + 32 * h < p.d)
+            emit_f32x32(&maps.out0, slot, lane, acc + 32 * h, col0 + 32 * h, p.v0 + wrow0, 0, false);
+      }
+    } else {
+      if (wrow0 >= p.n_rows) return;
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        if (col0 + 32 * h < p.d)
+          emit_f32x32(&maps.out1, slot, lane, acc + 32 * h, col0 + 32 * h, wrow0, j.split, p.dh_add != 0);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+// Persistent, one CTA pair per two SMs (cluster of 2, tcgen05 cta_group::2):
+//   warp 0      copies: this CTA's 128 rows of A and 128 of the tile's 256 B
+//               rows per stage, counted on the even CTA's barrier
+//   warp 1      (even CTA) issues the products, M = 256, N = 256, K = 16
+//   warps 2..9  epilogue: thread = row, each warp half of the columns
+// Two accumulators of 256 TMEM columns: the epilogue of one chunk runs beside
+// the products of the next.  Every wait is bounded (about one second).
+template <int ROLE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+    token_loss_kernel(const __grid_constant__ LossMaps maps, const LossParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + BAR_OFFSET);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* skip_word = tmem_slot + 2;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    // an earlier kernel of this call already gave up on a wait: skip the work
+    // (the even CTA decides for both)
+    *skip_word = *reinterpret_cast<volatile unsigned*>(p.err) & ERR_WAIT_TIMEOUT_MASK;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const bool skip = ld_cluster_u32(mapa_shared(smem_u32(skip_word), 0)) != 0;
+
+  const int nv = *p.n_valid;
+  const Jobs<ROLE> jobs(p, nv);
+  const int products = p.planes == 3 ? 6 : 1;
+  const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+
+  if (skip) {
+    // nothing to do
+  } else if (warp == 0) {
+    // ---------------- copies (both CTAs; whole warp, one elected lane issues) ----------------
+    const bool issuer = elect_one();
+    int stage = 0;
+    uint32_t phase = 0, armed = 0;
+    bool ok = true;
+    const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
+    for (int t = cid; t < jobs.total && ok; t += ncl) {
+      const Job j = jobs.get(p, nv, t);
+      const bool a_mn = ROLE == GRAD && j.dw, b_mn = ROLE == GRAD;
+      const CUtensorMap* ma = &maps.a;
+      const CUtensorMap* mb = ROLE == GRAD && j.dw ? &maps.c : &maps.b;
+      const int am = j.m0 + (int)rank * 128, bn = j.n0 + (int)rank * 128;
+      for (int q = 0; q < products && ok; ++q) {
+        const int ta = products == 1 ? 0 : term_a(q), tb = products == 1 ? 0 : term_b(q);
+        for (int kb = 0; kb < j.kblocks; ++kb) {
+          if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+          armed &= ~(1u << stage);
+          uint8_t* sa = smem + stage * STAGE_BYTES;
+          if (issuer) {
+            if (leader) mbar_expect_tx(&full[stage], 2 * STAGE_BYTES);   // both CTAs' copies
+            const uint32_t fb = full0 + (uint32_t)(stage * sizeof(uint64_t));
+            const int ka = j.ka + kb * BK, kbb = j.kb + kb * BK;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              tma_load_3d_pair(ma, fb, sa + h * BOX_BYTES, a_mn ? am + 64 * h : ka, a_mn ? ka : am + 64 * h, ta);
+              tma_load_3d_pair(mb, fb, sa + (2 + h) * BOX_BYTES, b_mn ? bn + 64 * h : kbb, b_mn ? kbb : bn + 64 * h,
+                               tb);
+            }
+          }
+          armed |= 1u << stage;
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+      }
+    }
+    if (!ok) {
+      if (issuer) atomicOr(p.err, 1u);
+      *abort_flag = 1;
+    }
+    if (*abort_flag && leader) {   // copies of both CTAs are counted on the even CTA's barriers
+      for (int s = 0; s < STAGES; ++s) {
+        if (!(armed & (1u << s))) continue;
+        const unsigned long long t0 = global_ns();
+        while (!mbar_try_wait_cluster(&full[s], 0) && !mbar_try_wait_cluster(&full[s], 1)) {
+          if (global_ns() - t0 > WAIT_LIMIT_NS) break;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (leader) {
+      // ---------------- products (even CTA; whole warp, one elected lane issues) ----------------
+      const bool issuer = elect_one();
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = cid; t < jobs.total && ok; t += ncl) {
+        const Job j = jobs.get(p, nv, t);
+        const bool a_mn = ROLE == GRAD && j.dw, b_mn = ROLE == GRAD;
+        const uint32_t idesc = idesc_f16(TILE, 1, TILE) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+        const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
+        const int iters = products * j.kblocks;
+        for (int it = 0; it < iters && ok;) {
+          if (!mbar_wait_cluster_warp(&tempty[buf], acc_phase ^ 1, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + (uint32_t)(buf * TILE);
+          const int end = min(iters, it + p.chunk);
+          for (int first = it; it < end; ++it) {
+            if (!mbar_wait_cluster_warp(&full[stage], phase, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
+            const uint32_t sb = sa + 2 * BOX_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk)
+              if (issuer)
+                mma_f16_pair(d_tmem, operand_desc(sa + kk * step_a, a_mn), operand_desc(sb + kk * step_b, b_mn), idesc,
+                             (it > first || kk > 0) ? 1u : 0u);
+            if (issuer) mma_commit_pair(&empty[stage], 0x3);
+            if (++stage == STAGES) { stage = 0; phase ^= 1; }
+          }
+          if (!ok) break;
+          if (issuer) mma_commit_pair(&tfull[buf], 0x3);
+          if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+        }
+      }
+      if (!ok) {
+        if (issuer) atomicOr(p.err, 2u);
+        *abort_flag = 1;
+      }
+      if (issuer) mma_commit_pair(drain, 0x1);   // no product writes either CTA's TMEM after this arrives
+      const unsigned long long t0 = global_ns();
+      while (!mbar_try_wait(drain, 0)) {
+        if (global_ns() - t0 > WAIT_LIMIT_NS) break;
+      }
+    }
+  } else {
+    // ---------------- epilogue (warps 2..9, both CTAs) ----------------
+    const int quarter = warp & 3;
+    const int half = (warp - 2) >> 2;
+    const int row_in_tile = (int)rank * 128 + quarter * 32 + lane;
+    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    uint8_t* slot = smem + SLOT_OFFSET + (warp - 2) * SLOT_BYTES;
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int t = cid; t < jobs.total && ok; t += ncl) {
+      const Job j = jobs.get(p, nv, t);
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      const int iters = products * j.kblocks;
+      for (int it = 0; it < iters; it += p.chunk) {
+        const bool got = mbar_wait_cluster(&tfull[buf], acc_phase, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) {
+          if (lane == 0) atomicOr(p.err, 4u);
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * TILE + half * 128);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          tmem_ld32(tbase + (uint32_t)(c * 32), v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[c * 32 + i] += v[i];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
+        if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+      }
+      if (ok) finish_tile<ROLE>(p, maps, j, nv, acc, row_in_tile, half, lane, slot);
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  cluster_sync_all();   // no product, copy or epilogue of either CTA still uses TMEM or shared memory
+  tc_fence_after();
+  if (warp == 1) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Row order: rows with a target first, in their order; the others fill the
+// end backwards.  Copies the hidden rows there as bf16 (fp32 rows as three
+// terms); rows without a target are written as zeros.
+struct RowParams {
+  int n, d, vocab, rows_per_block;
+  int clear_err;
+  const void* targets; int target_bytes;
+  const void* hidden;
+  bf16* rows;                 // [planes][n][d]
+  int* perm; int* target; int* n_valid;
+  // gradient: weights divided by the largest magnitude (so that a weight that
+  // is the same for all rows leaves P at exact multiples), lse gathered
+  const float* d_loss; const float* lse_in; float* g; float* lse; float* g_max;
+  // loss: outputs of rows without a target
+  float* loss_out; float* lse_out;
+  unsigned* err;
+};
+
+__device__ __forceinline__ void split3(float x, bf16& hi, bf16& mid, bf16& lo) {
+  hi = __float2bfloat16_rn(x);
+  const float r = x - __bfloat162float(hi);
+  mid = __float2bfloat16_rn(r);
+  lo = __float2bfloat16_rn(r - __bfloat162float(mid));
+  if (!isfinite(__bfloat162float(hi))) mid = lo = __float2bfloat16_rn(0.f);   // inf - inf would be NaN
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
+  __shared__ int s_count[8];
+  __shared__ float s_max[8];
+  __shared__ int s_slot[64];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = blockIdx.x * p.rows_per_block;
+  const int nr = min(p.rows_per_block, p.n - r0);
+  auto valid = [&](int i) {
+    const long long t = load_id(p.targets, p.target_bytes, i);
+    return t >= 0 && t < p.vocab;
+  };
+  int before = 0;
+  float gm = 0.f;
+  const int scan = p.d_loss ? p.n : r0;
+  for (int i = threadIdx.x; i < scan; i += 256) {
+    const bool ok = valid(i);
+    if (ok && i < r0) ++before;
+    if (ok && p.d_loss) {
+      const float g = fabsf(p.d_loss[i]);
+      gm = (g > gm || g != g) ? g : gm;   // keeps a NaN
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    const float y = __shfl_xor_sync(0xffffffffu, gm, o);
+    gm = (y > gm || y != y) ? y : gm;
+  }
+  if (lane == 0) { s_count[warp] = before; s_max[warp] = gm; }
+  __syncthreads();
+  before = 0;
+  gm = 0.f;
+  for (int w = 0; w < 8; ++w) {
+    before += s_count[w];
+    const float y = s_max[w];
+    gm = (y > gm || y != y) ? y : gm;
+  }
+  if (threadIdx.x == 0 && blockIdx.x == 0) {
+    if (p.clear_err) *p.err = 0;
+    if (p.d_loss) *p.g_max = gm;
+  }
+  if (warp == 0) {
+    int seen = before;
+    for (int b = 0; b < nr; b += 32) {
+      const int i = r0 + b + lane;
+      const bool here = b + lane < nr;
+      const bool ok = here && valid(i);
+      const unsigned mask = __ballot_sync(0xffffffffu, ok);
+      const int vb = seen + __popc(mask & ((1u << lane) - 1));   // rows with a target before row i
+      if (here) {
+        const int at = ok ? vb : p.n - 1 - (i - vb);
+        s_slot[b + lane] = ok ? at : ~at;
+        p.perm[at] = i;
+        p.target[at] = ok ? (int)load_id(p.targets, p.target_bytes, i) : -1;
+        if (p.d_loss) {
+          p.g[at] = ok && gm != 0.f ? p.d_loss[i] / gm : 0.f;
+          p.lse[at] = ok ? p.lse_in[i] : 0.f;
+        }
+        if (p.loss_out && !ok) {
+          p.loss_out[i] = 0.f;
+          p.lse_out[i] = 0.f;
+        }
+      }
+      seen += __popc(mask);
+    }
+    if (r0 + nr == p.n && lane == 0) *p.n_valid = seen;
+  }
+  __syncthreads();
+  const int vecs = p.d / 8;   // 8 elements per step
+  const long long plane = (long long)p.n * p.d;
+  for (int k = threadIdx.x; k < nr * vecs; k += 256) {
+    const int r = k / vecs, c = (k - r * vecs) * 8;
+    const int at = s_slot[r];
+    const bool ok = at >= 0;
+    bf16* dst = p.rows + (long long)(ok ? at : ~at) * p.d + c;
+    if constexpr (sizeof(T) == 2) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (ok) x = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.hidden) + (long long)(r0 + r) * p.d + c);
+      *reinterpret_cast<uint4*>(dst) = x;
+    } else {
+      const float* src = reinterpret_cast<const float*>(p.hidden) + (long long)(r0 + r) * p.d + c;
+      __align__(16) bf16 t[3][8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) split3(ok ? src[i] : 0.f, t[0][i], t[1][i], t[2][i]);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(dst + q * plane) = *reinterpret_cast<uint4*>(t[q]);
+    }
+  }
+}
+
+// fp32 head as three bf16 terms: out[3][n], n a multiple of 8.
+__global__ void __launch_bounds__(256) split_terms_kernel(const float* x, bf16* out, long long n) {
+  for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (long long)gridDim.x * 256 * 8) {
+    __align__(16) bf16 t[3][8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) split3(x[i + k], t[0][k], t[1][k], t[2][k]);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(out + q * n + i) = *reinterpret_cast<uint4*>(t[q]);
+  }
+}
+
+// Joins the tiles' (max, sum) of each row: rb rows per block, 1024 / rb
+// threads share a row's tiles and meet in shared memory.  The order of the
+// sums is fixed.
+__global__ void __launch_bounds__(1024) join_lse_kernel(const float2* part, int part_pitch, int n_parts,
+                                                        const float* target_logit, const int* n_valid, const int* perm,
+                                                        int rb, float* loss, float* lse, const unsigned* err) {
+  __shared__ float2 s[1024];
+  const int x = threadIdx.x % rb, y = threadIdx.x / rb, ny = 1024 / rb;
+  const int row = blockIdx.x * rb + x;
+  const bool in = row < *n_valid;
+  float m = -INFINITY, sum = 0.f;
+  auto add = [&](float2 o) {
+    const float nm = fmaxf(m, o.x);
+    const float base = nm == -INFINITY ? 0.f : nm;
+    sum = sum * ex2((m - base) * LOG2E) + o.y * ex2((o.x - base) * LOG2E);
+    m = nm;
+  };
+  if (in) {
+#pragma unroll 4
+    for (int i = y; i < n_parts; i += ny) add(part[(long long)i * part_pitch + row]);
+  }
+  s[threadIdx.x] = make_float2(m, sum);
+  __syncthreads();
+  for (int h = ny / 2; h; h >>= 1) {
+    if (y < h) {
+      add(s[threadIdx.x + h * rb]);
+      s[threadIdx.x] = make_float2(m, sum);
+    }
+    __syncthreads();
+  }
+  if (y == 0 && in) {
+    const float ls = logf(sum);
+    const bool bad = *err != 0;
+    loss[perm[row]] = bad ? NAN : (m - target_logit[row]) + ls;
+    lse[perm[row]] = bad ? NAN : m + ls;
+  }
+}
+
+// dH rows back in their order: the splits' partial sums added in order, times
+// the weights' common factor.  After a wait that ran out, NaN.
+template <typename T>
+__global__ void __launch_bounds__(256) join_rows_kernel(const float* part, int splits, int n, int d, const int* perm,
+                                                        const int* n_valid, const float* g_max, float scale,
+                                                        const unsigned* err, T* out) {
+  const int nv = *n_valid;
+  const bool bad = *err != 0;
+  const float f = *g_max * scale;
+  const int vecs = d / 8;
+  const long long total = (long long)n * vecs, plane = (long long)n * d;
+  for (long long k = (long long)blockIdx.x * 256 + threadIdx.x; k < total; k += (long long)gridDim.x * 256) {
+    const int r = (int)(k / vecs), c = (int)(k - (long long)r * vecs) * 8;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = bad ? NAN : 0.f;
+    if (r < nv && !bad) {
+      for (int s = 0; s < splits; ++s) {
+        const float4* src = reinterpret_cast<const float4*>(part + s * plane + (long long)r * d + c);
+        const float4 a = src[0], b = src[1];
+        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= f;
+    }
+    T* dst = out + (long long)perm[r] * d + c;
+    if constexpr (sizeof(T) == 2) {
+      __align__(16) bf16 t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = __float2bfloat16_rn(v[i]);
+      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<uint4*>(t);
+    } else {
+      reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
+}
+
+// After a wait that ran out: NaN in the head's gradient too.
+template <typename T>
+__global__ void __launch_bounds__(256) fail_head_kernel(const unsigned* err, T* out, long long n) {
+  if (*err == 0) return;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256)
+    out[i] = (T)NAN;
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+
+constexpr int LOSS_ROWS = 8192;                    // rows per forward pass: bounds the (max, sum) workspace
+constexpr long long P_BYTES = 256ll << 20;         // P of one vocabulary piece
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+int round_up(int a, int b) { return (a + b - 1) / b * b; }
+int div_up(int a, int b) { return (a + b - 1) / b; }
+
+// Workspace of one call, laid out in order.
+struct Layout {
+  int planes, rows, pieces, vc, splits, k_split, n_parts;
+  size_t n_valid, g_max, rows_b, perm, target, g, lse, tlogit, part, head, p, dh, total;
+  Layout(int n, int v, int d, bool f32, bool grad) {
+    planes = f32 ? 3 : 1;
+    rows = grad ? n : (n < LOSS_ROWS ? n : LOSS_ROWS);
+    n_parts = 2 * div_up(v, TILE);
+    vc = v; pieces = 1; splits = k_split = 0;
+    if (grad) {
+      long long w = P_BYTES / ((long long)n * 2 * planes) / TILE * TILE;
+      if (w < TILE) w = TILE;
+      if (w < v) {
+        pieces = div_up(v, (int)w);
+        vc = round_up(div_up(v, pieces), TILE);
+        pieces = div_up(v, vc);
+      }
+      // dH tiles contract over the piece in splits of about the length of dW's
+      // contraction, so that the tiles of a launch are alike; more and shorter
+      // ones where there are few rows
+      const long long want = 4ll * n;
+      const int ks = (int)(want < 2048 ? 2048 : (want > 8192 ? 8192 : want));
+      splits = div_up(vc, ks);
+      k_split = round_up(div_up(vc, splits), BK);
+      splits = div_up(vc, k_split);
+    }
+    size_t o = 256;   // the error word
+    auto take = [&](size_t bytes) { const size_t at = o; o += up256(bytes); return at; };
+    n_valid = take(4);
+    g_max = take(4);
+    rows_b = take((size_t)planes * rows * d * 2);
+    perm = take((size_t)rows * 4);
+    target = take((size_t)rows * 4);
+    g = take(grad ? (size_t)rows * 4 : 0);
+    lse = take(grad ? (size_t)rows * 4 : 0);
+    tlogit = take(grad ? 0 : (size_t)rows * 4);
+    part = take(grad ? 0 : (size_t)n_parts * rows * 8);
+    head = take(f32 ? (size_t)3 * v * d * 2 : 0);
+    p = take(grad ? (size_t)planes * n * round_up(vc, 64) * 2 : 0);
+    dh = take(grad ? (size_t)splits * n * d * 4 : 0);
+    total = o;
+  }
+};
+
+// [outer][rows][inner] with rows `pitch` elements apart, box box_inner x box_rows, 128-byte swizzle.
+cudaError_t make_map(CUtensorMap* map, const void* base, bool f32, int inner, long long pitch, int rows, int outer,
+                     int box_inner, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = get_tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t esz = f32 ? 4 : 2;
+  cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)outer};
+  cuuint64_t strides[2] = {(cuuint64_t)pitch * esz, (cuuint64_t)pitch * rows * esz};
+  cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t load_map(CUtensorMap* map, const void* base, int inner, long long pitch, int rows, int outer) {
+  return make_map(map, base, false, inner, pitch, rows, outer, BK, 64);
+}
+
+// Pairs of CTAs the device runs at once, per device (set up on first use).
+template <int ROLE>
+cudaError_t pairs_on_device(int* out) {
+  constexpr int MAX_DEVICES = 64;
+  static std::mutex mu;
+  static int known[MAX_DEVICES] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= MAX_DEVICES) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!known[dev]) {
+    e = cudaFuncSetAttribute(token_loss_kernel<ROLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM_TOTAL;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2; attr.val.clusterDim.y = 1; attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, token_loss_kernel<ROLE>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    known[dev] = n;
+  }
+  *out = known[dev];
+  return cudaSuccess;
+}
+
+template <int ROLE>
+cudaError_t launch_products(const LossMaps& maps, const LossParams& p, long long jobs, cudaStream_t st) {
+  int pairs = 0;
+  cudaError_t e = pairs_on_device<ROLE>(&pairs);
+  if (e != cudaSuccess) return e;
+  const int grid = (int)(jobs < pairs ? jobs : pairs);
+  token_loss_kernel<ROLE><<<2 * grid, NUM_THREADS, SMEM_TOTAL, st>>>(maps, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_order_rows(RowParams rp, bool f32, cudaStream_t st) {
+  rp.rows_per_block = rp.n <= 16384 ? 16 : 64;   // blocks scan the targets before them: fewer blocks for many rows
+  const int grid = div_up(rp.n, rp.rows_per_block);
+  if (f32) order_rows_kernel<float><<<grid, 256, 0, st>>>(rp);
+  else order_rows_kernel<bf16><<<grid, 256, 0, st>>>(rp);
+  return cudaGetLastError();
+}
+
+// The head as the products read it: bf16 as it is, fp32 as three terms.
+cudaError_t head_operand(const Layout& L, char* ws, const void* head, int v, int d, bool f32, const void** out,
+                         cudaStream_t st) {
+  *out = head;
+  if (!f32) return cudaSuccess;
+  const long long n = (long long)v * d;
+  const long long blocks = (n / 8 + 255) / 256;
+  split_terms_kernel<<<(int)(blocks < 148 * 16 ? blocks : 148 * 16), 256, 0, st>>>((const float*)head,
+                                                                                (bf16*)(ws + L.head), n);
+  *out = ws + L.head;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+}  // namespace armt
+
+using namespace armt;
+
+extern "C" armt_status armt_token_loss_workspace(armt_dtype dtype, int n, int vocab, int d, int grad, size_t* bytes) {
+  if (!bytes) return ARMT_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (grad != 0 && grad != 1) return ARMT_ERR_INVALID_ARG;
+  const armt_status s = check_sizes(dtype, n, vocab, d);
+  if (s != ARMT_OK) return s;
+  *bytes = Layout(n, vocab, d, dtype == ARMT_FP32, grad != 0).total;
+  return ARMT_OK;
+}
+
+extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d, const void* hidden, const void* head,
+                                       const void* targets, int target_bytes, float scale, float* loss, float* lse,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  armt_status s = check_sizes(dtype, n, vocab, d);
+  if (s != ARMT_OK) return s;
+  if (!hidden || !head || !targets || !loss || !lse || !workspace || !std::isfinite(scale) ||
+      (target_bytes != 4 && target_bytes != 8) || !aligned16(hidden) || !aligned16(head) || !aligned16(workspace))
+    return ARMT_ERR_INVALID_ARG;
+  const bool f32 = dtype == ARMT_FP32;
+  const Layout L(n, vocab, d, f32, false);
+  if (workspace_bytes < L.total) return ARMT_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  char* ws = (char*)workspace;
+  const void* w = nullptr;
+  cudaError_t e = head_operand(L, ws, head, vocab, d, f32, &w, st);
+  LossMaps maps{};
+  if (e == cudaSuccess) e = load_map(&maps.b, w, d, d, vocab, L.planes);
+  for (int r0 = 0; r0 < n && e == cudaSuccess; r0 += L.rows) {
+    const int nr = n - r0 < L.rows ? n - r0 : L.rows;
+    RowParams rp{};
+    rp.n = nr; rp.d = d; rp.vocab = vocab; rp.clear_err = r0 == 0;
+    rp.targets = (const char*)targets + (size_t)r0 * target_bytes; rp.target_bytes = target_bytes;
+    rp.hidden = (const char*)hidden + (size_t)r0 * d * (f32 ? 4 : 2);
+    rp.rows = (bf16*)(ws + L.rows_b); rp.perm = (int*)(ws + L.perm); rp.target = (int*)(ws + L.target);
+    rp.n_valid = (int*)(ws + L.n_valid); rp.err = (unsigned*)ws;
+    rp.loss_out = loss + r0; rp.lse_out = lse + r0;
+    e = launch_order_rows(rp, f32, st);
+    if (e == cudaSuccess) e = load_map(&maps.a, ws + L.rows_b, d, d, nr, L.planes);
+    if (e != cudaSuccess) break;
+    LossParams p{};
+    p.n_rows = nr; p.d = d; p.vocab = vocab; p.planes = L.planes; p.v0 = 0; p.vc = vocab;
+    p.chunk = LOGIT_CHUNK; p.scale = scale; p.n_valid = rp.n_valid; p.target = rp.target;
+    p.part = (float2*)(ws + L.part); p.part_pitch = nr; p.target_logit = (float*)(ws + L.tlogit); p.err = rp.err;
+    e = launch_products<LSE>(maps, p, (long long)div_up(nr, TILE) * div_up(vocab, TILE), st);
+    if (e != cudaSuccess) break;
+    int rb = 32;
+    while (rb > 1 && rb / 2 >= nr) rb /= 2;
+    join_lse_kernel<<<div_up(nr, rb), 1024, 0, st>>>(p.part, nr, L.n_parts, p.target_logit, rp.n_valid, rp.perm, rb,
+                                                     loss + r0, lse + r0, rp.err);
+    e = cudaGetLastError();
+  }
+  return cuda_status(e);
+}
+
+extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, int d, const void* hidden,
+                                            const void* head, const void* targets, int target_bytes, float scale,
+                                            const float* lse, const float* d_loss, void* d_hidden, void* d_head,
+                                            void* workspace, size_t workspace_bytes, void* stream) {
+  armt_status s = check_sizes(dtype, n, vocab, d);
+  if (s != ARMT_OK) return s;
+  if (!hidden || !head || !targets || !lse || !d_loss || (!d_hidden && !d_head) || !workspace ||
+      !std::isfinite(scale) || (target_bytes != 4 && target_bytes != 8) || !aligned16(hidden) || !aligned16(head) ||
+      !aligned16(workspace) || !aligned16(d_hidden) || !aligned16(d_head))
+    return ARMT_ERR_INVALID_ARG;
+  const bool f32 = dtype == ARMT_FP32;
+  const Layout L(n, vocab, d, f32, true);
+  if (workspace_bytes < L.total) return ARMT_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  char* ws = (char*)workspace;
+  const void* w = nullptr;
+  cudaError_t e = head_operand(L, ws, head, vocab, d, f32, &w, st);
+  RowParams rp{};
+  rp.n = n; rp.d = d; rp.vocab = vocab; rp.clear_err = 1;
+  rp.targets = targets; rp.target_bytes = target_bytes; rp.hidden = hidden;
+  rp.rows = (bf16*)(ws + L.rows_b); rp.perm = (int*)(ws + L.perm); rp.target = (int*)(ws + L.target);
+  rp.n_valid = (int*)(ws + L.n_valid); rp.err = (unsigned*)ws;
+  rp.d_loss = d_loss; rp.lse_in = lse; rp.g = (float*)(ws + L.g); rp.lse = (float*)(ws + L.lse);
+  rp.g_max = (float*)(ws + L.g_max);
+  if (e == cudaSuccess) e = launch_order_rows(rp, f32, st);
+  LossMaps mp{}, mg{};   // PROB, GRAD
+  if (e == cudaSuccess) e = load_map(&mp.a, ws + L.rows_b, d, d, n, L.planes);
+  if (e == cudaSuccess) e = load_map(&mp.b, w, d, d, vocab, L.planes);
+  mg.b = mp.b;
+  mg.c = mp.a;
+  if (e == cudaSuccess && d_head) e = make_map(&mg.out0, d_head, f32, d, d, vocab, 1, f32 ? 32 : 64, 32);
+  if (e == cudaSuccess && d_hidden) e = make_map(&mg.out1, ws + L.dh, true, d, d, n, L.splits, 32, 32);
+  LossParams p{};
+  p.n_rows = n; p.d = d; p.vocab = vocab; p.planes = L.planes; p.scale = scale;
+  p.n_valid = rp.n_valid; p.target = rp.target; p.lse = rp.lse; p.g = rp.g; p.g_max = rp.g_max; p.err = rp.err;
+  p.want_dw = d_head != nullptr; p.want_dh = d_hidden != nullptr; p.dw_bf16 = !f32; p.k_split = L.k_split;
+  const int pitch = round_up(L.vc, 64), mt = div_up(n, TILE), dt = div_up(d, TILE);
+  for (int v0 = 0; v0 < vocab && e == cudaSuccess; v0 += L.vc) {
+    p.v0 = v0;
+    p.vc = vocab - v0 < L.vc ? vocab - v0 : L.vc;
+    p.splits = div_up(p.vc, L.k_split);
+    p.dh_add = v0 > 0;
+    e = load_map(&mg.a, ws + L.p, p.vc, pitch, n, L.planes);
+    if (e == cudaSuccess) e = make_map(&mp.out0, ws + L.p, false, p.vc, pitch, n, L.planes, 64, 32);
+    p.chunk = LOGIT_CHUNK;
+    const int nt = div_up(p.vc, TILE);
+    if (e == cudaSuccess) e = launch_products<PROB>(mp, p, (long long)mt * nt, st);
+    p.chunk = f32 ? LOGIT_CHUNK : 1 << 30;   // bf16 results: one accumulator over the whole contraction
+    const long long jobs = (p.want_dw ? (long long)nt * dt : 0) + (p.want_dh ? (long long)mt * dt * p.splits : 0);
+    if (e == cudaSuccess) e = launch_products<GRAD>(mg, p, jobs, st);
+  }
+  if (e == cudaSuccess && d_hidden) {
+    const long long blocks = ((long long)n * (d / 8) + 255) / 256;
+    const int grid = (int)(blocks < 148 * 16 ? blocks : 148 * 16);
+    const float* part = (const float*)(ws + L.dh);
+    if (f32)
+      join_rows_kernel<float><<<grid, 256, 0, st>>>(part, L.splits, n, d, rp.perm, rp.n_valid, rp.g_max, scale, rp.err,
+                                                    (float*)d_hidden);
+    else
+      join_rows_kernel<bf16><<<grid, 256, 0, st>>>(part, L.splits, n, d, rp.perm, rp.n_valid, rp.g_max, scale, rp.err,
+                                                   (bf16*)d_hidden);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess && d_head) {
+    const long long total = (long long)vocab * d;
+    if (f32) fail_head_kernel<float><<<148, 256, 0, st>>>(rp.err, (float*)d_head, total);
+    else fail_head_kernel<bf16><<<148, 256, 0, st>>>(rp.err, (bf16*)d_head, total);
+    e = cudaGetLastError();
+  }
+  return cuda_status(e);
+}
+
+// Read by the host after the stream has finished: whether a bounded wait ran
+// out in the last call that used this workspace.
+extern "C" armt_status armt_workspace_status(const void* workspace, void* stream) {
+  if (!workspace) return ARMT_ERR_INVALID_ARG;
+  unsigned err = 0;
+  cudaError_t e = cudaMemcpyAsync(&err, workspace, sizeof(err), cudaMemcpyDeviceToHost, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_status(e);
+  return err ? ARMT_ERR_DEVICE_TIMEOUT : ARMT_OK;
+}

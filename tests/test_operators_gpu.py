@@ -1,0 +1,563 @@
+"""The operators at the ends of the model against plain 64-bit implementations.
+
+Tolerances are bounds per element, from the roundings that the formulas and the
+kernels' order of sums allow (u = 2^-24, half a step of fp32; h = half a step of
+the type), not measured figures.
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float32
+U = 2.0 ** -24
+
+
+def half(t):
+    return torch.finfo(t).eps / 2
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, *s):
+    return torch.randn(*s, generator=g, device="cuda")
+
+
+def check(got, want, tol, what=""):
+    """|got - want| <= tol for every element (and finite where want is)."""
+    d = (got.double() - want).abs()
+    bad = ~(d <= tol)
+    assert not bad.any(), (what, int(bad.sum()), float((d / tol.clamp(min=1e-300)).max()))
+
+
+# ------------------------------------------------------------------ embedding
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n,v,d,idt", [(1, 1, 8, torch.int64), (3, 7, 8, torch.int32), (67, 515, 64, torch.int64),
+                                       (1025, 33, 2056, torch.int32), (4099, 50021, 256, torch.int64)])
+def test_embed(n, v, d, idt, dtype):
+    from recurrent_memory_transformer_diag_b200 import embed
+    g = gen(n + v)
+    table = randn(g, v, d).to(dtype)
+    ids = torch.randint(-2, v + 2, (n,), generator=g, device="cuda").to(idt)
+    if n > 1:
+        ids[0] = -1
+    scale = 1.7
+    out = torch.full((n, d), float("nan"), dtype=dtype, device="cuda")
+    embed(ids, table, out, scale=scale)
+    ok = (ids >= 0) & (ids < v)
+    want = torch.where(ok[:, None], table.double()[ids.long().clamp(0, v - 1)] * scale, 0.0)
+    # the scale as fp32, the product in fp32, then the type
+    check(out, want, want.abs() * (half(dtype) + 2.5 * U) + 1e-38)
+    embed(ids, table, out)   # scale 1: a copy
+    assert torch.equal(out, torch.where(ok[:, None], table[ids.long().clamp(0, v - 1)], torch.zeros_like(out)))
+
+
+def grad_reference(ids, d_out, v, scale, base):
+    ok = (ids >= 0) & (ids < v)
+    i, x = ids[ok].long(), d_out[ok].double()
+    z = torch.zeros(v, d_out.shape[1], dtype=torch.float64, device="cuda")
+    s, a = z.index_add(0, i, x) * scale, z.index_add(0, i, x.abs()) * abs(scale)
+    count = torch.bincount(i, minlength=v).double()[:, None]
+    return s + base, a, count
+
+
+EMBED_GRAD = [
+    # n, v, d, how the ids fall
+    (1, 1, 8, "uniform"), (1, 300, 64, "uniform"), (67, 515, 64, "uniform"),
+    (2048, 1000, 72, "skewed"),            # most tokens of the one-launch form
+    (2048, 40, 64, "one"),
+    (2049, 1000, 72, "skewed"),            # fewest of the sorted one
+    (2049, 1, 8, "uniform"),               # one row takes everything
+    (5000, 511, 64, "uniform"), (5000, 512, 64, "uniform"), (5000, 262145, 8, "uniform"),   # 1, 2, 3 passes
+    (20011, 3001, 256, "skewed"), (9000, 100, 2048, "one"), (6400, 100, 64, "blocks"),
+    (4097, 77, 2056, "skewed"),            # columns in two blocks
+    (3000, 50, 16, "none"),
+]
+
+
+def make_ids(g, n, v, how):
+    if how == "uniform":
+        return torch.randint(0, v, (n,), generator=g, device="cuda")
+    if how == "one":
+        return torch.full((n,), v // 2, device="cuda", dtype=torch.int64)
+    if how == "none":
+        return torch.full((n,), -1, device="cuda", dtype=torch.int64)
+    if how == "blocks":   # runs that end exactly at multiples of 64
+        return (torch.arange(n, device="cuda") // 64) % v
+    ids = (v * torch.rand(n, generator=g, device="cuda") ** 4).long().clamp_(max=v - 1)
+    ids[torch.rand(n, generator=g, device="cuda") < 0.1] = -100
+    return ids
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n,v,d,how", EMBED_GRAD)
+def test_embed_grad(n, v, d, how, dtype, accumulate):
+    from recurrent_memory_transformer_diag_b200 import embed_grad
+    g = gen(n + v + d)
+    ids = make_ids(g, n, v, how)
+    d_out = randn(g, n, d).to(dtype)
+    base = randn(g, v, d).to(dtype)
+    scale = 0.75
+    out = base.clone() if accumulate else torch.full_like(base, float("nan"))
+    embed_grad(ids, d_out, out, scale=scale, accumulate=accumulate)
+    want, absum, count = grad_reference(ids, d_out, v, scale, base.double() if accumulate else 0.0)
+    # a sum of k terms in any fixed order, the scale, the base, the type
+    check(out, want, absum * (count + 3) * U + want.abs() * (half(dtype) + U) + 1e-38)
+    if accumulate:   # rows that no token names keep their bits
+        assert torch.equal(out[count[:, 0] == 0], base[count[:, 0] == 0])
+    again = base.clone() if accumulate else torch.empty_like(base)
+    embed_grad(ids.to(torch.int32), d_out, again, scale=scale, accumulate=accumulate)
+    assert torch.equal(again, out)   # no order left to chance; int32 ids alike
+
+
+def test_embed_grad_is_the_gradient_of_embed():
+    """<d_out, embed(table + e) - embed(table)> = <d_table, e> for exact values
+    (small integers: every sum below 2^24 is exact)."""
+    from recurrent_memory_transformer_diag_b200 import embed, embed_grad
+    g = gen(5)
+    n, v, d = 3001, 97, 40
+    table = torch.randint(-8, 9, (v, d), generator=g, device="cuda").float()
+    e = torch.randint(-3, 4, (v, d), generator=g, device="cuda").float()
+    d_out = torch.randint(-4, 5, (n, d), generator=g, device="cuda").float()
+    ids = torch.randint(-1, v, (n,), generator=g, device="cuda")
+    a, b = torch.empty(n, d, device="cuda"), torch.empty(n, d, device="cuda")
+    embed(ids, table, a, scale=2.0)
+    embed(ids, table + e, b, scale=2.0)
+    d_table = torch.empty(v, d, device="cuda")
+    embed_grad(ids, d_out, d_table, scale=2.0)
+    assert float((d_out.double() * (b - a).double()).sum()) == float((d_table.double() * e.double()).sum())
+
+
+def test_embed_masked_values():
+    """NaN and infinities of padding rows do not reach the table's gradient."""
+    from recurrent_memory_transformer_diag_b200 import embed_grad
+    for n in (100, 4000):
+        ids = torch.arange(n, device="cuda") % 13
+        ids[::3] = -1
+        d_out = torch.ones(n, 16, device="cuda")
+        d_out[::3] = float("nan")
+        d_out[0] = float("inf")
+        out = torch.empty(20, 16, device="cuda")
+        embed_grad(ids, d_out, out)
+        want = torch.bincount(ids[ids >= 0], minlength=20).double()[:, None].expand(20, 16)
+        assert torch.equal(out.double(), want)
+
+
+# ------------------------------------------------------------------ norm
+NORM = [(1, 8), (7, 64), (33, 256), (5, 264), (9, 1000), (65, 2048), (11, 2056), (3, 4096), (4, 8192), (2, 16384),
+        (3000, 512), (700, 2048)]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n,d", NORM)
+def test_rms_norm_and_gradient(n, d, dtype):
+    from recurrent_memory_transformer_diag_b200 import rms_norm, rms_norm_grad
+    g = gen(n + d)
+    x = (randn(g, n, d) * torch.exp(2 * randn(g, n, 1))).to(dtype)
+    gain = (1 + 0.3 * randn(g, d)).to(dtype)
+    dy = randn(g, n, d).to(dtype)
+    eps = 1e-5
+    y, rstd = torch.empty_like(x), torch.empty(n, device="cuda")
+    rms_norm(x, gain, y, rstd, eps)
+    X, G, D = x.double(), gain.double(), dy.double()
+    R = ((X * X).mean(1, keepdim=True) + eps) ** -0.5
+    # a lane adds at most d / 32 squares, then 5 + 8 sums; half of that reaches the root, plus rsqrt's 2 ulp
+    er = (d / 32 + 16) * U / 2 + 6 * U
+    check(rstd[:, None], R, R * er)
+    Y = X * R * G
+    check(y, Y, Y.abs() * (er + 3 * U + half(dtype)) + 1e-38)
+    dx, d_gain = torch.full_like(x, float("nan")), torch.full_like(gain, float("nan"))
+    rms_norm_grad(x, gain, rstd, dy, dx, d_gain)
+    M = (D * G * X).mean(1, keepdim=True)
+    Ma = (D * G * X).abs().mean(1, keepdim=True)
+    want = R * (D * G - X * R * R * M)
+    mag = R * ((D * G).abs() + X.abs() * R * R * Ma)
+    check(dx, want, mag * (3 * er + (d / 32 + 16) * U + 8 * U) + want.abs() * half(dtype) + 1e-38)
+    wg = (D * X * R).sum(0)
+    mag = (D * X * R).abs().sum(0)
+    # a block's warp adds its rows, 8 warps, at most 10 partial sums in a group, 32 groups
+    check(d_gain, wg, mag * (er + (n / 8 + 8 + 10 + 32 + 3) * U) + wg.abs() * half(dtype) + 1e-38)
+    # in place
+    y2, dx2 = x.clone(), dy.clone()
+    rms_norm(y2, gain, y2, None, eps)
+    assert torch.equal(y2, y)
+    rms_norm_grad(x, gain, rstd, dx2, dx2, torch.empty_like(gain))
+    assert torch.equal(dx2, dx)
+
+
+def test_rms_norm_zero_row():
+    from recurrent_memory_transformer_diag_b200 import rms_norm, rms_norm_grad
+    x = torch.zeros(3, 64, device="cuda")
+    x[1] = 1.0
+    gain = torch.ones(64, device="cuda")
+    y, rstd = torch.empty_like(x), torch.empty(3, device="cuda")
+    rms_norm(x, gain, y, rstd, 1e-6)
+    assert torch.equal(y[0], x[0]) and torch.allclose(rstd[0], torch.tensor(1e3, device="cuda"))
+    dx, dg = torch.empty_like(x), torch.empty_like(gain)
+    rms_norm_grad(x, gain, rstd, torch.ones_like(x), dx, dg)
+    assert torch.isfinite(dx).all() and torch.allclose(dx[0], torch.full((64,), 1e3, device="cuda"))
+
+
+# ------------------------------------------------------------------ vocabulary loss
+def loss_reference(hidden, head, targets, scale):
+    """logits, lse, loss, sum |h w| (64 bits), and which rows count."""
+    H, W = hidden.double(), head.double()
+    ok = (targets >= 0) & (targets < head.shape[0])
+    H = torch.where(ok[:, None], H, 0.0)
+    L = H @ W.t() * scale
+    lse = torch.logsumexp(L, 1)
+    t = targets.long().clamp(0, head.shape[0] - 1)[:, None]
+    loss = torch.where(ok, lse - L.gather(1, t)[:, 0], 0.0)
+    A = (H.abs() @ W.abs().t()).max(1).values * abs(scale)
+    return L, torch.where(ok, lse, 0.0), loss, A, ok
+
+
+def logit_error(A, d, planes):
+    """A logit's error: a chunk of at most 16 instructions, each truncated (2 u) once in the
+    instruction's own sum and once in the accumulator, chunks added to nearest; fp32 operands:
+    six products, and three terms of 24 bits less what the dropped products hold."""
+    terms = 6 if planes == 3 else 1
+    chunks = math.ceil(terms * math.ceil(d / 64) / 4)
+    return A * ((32 * 2 + chunks) * U + (8 * U if planes == 3 else 0))
+
+
+def loss_inputs(seed, n, v, d, dtype, idt=torch.int64, ignored=0.2):
+    g = gen(seed)
+    head = (randn(g, v, d) / math.sqrt(d)).to(dtype)
+    t = torch.randint(0, v, (n,), generator=g, device="cuda")
+    hidden = (randn(g, n, d) + 8 * torch.rand(n, 1, generator=g, device="cuda") * head[t].float()).to(dtype)
+    t[torch.rand(n, generator=g, device="cuda") < ignored] = -100
+    w = (0.5 + torch.rand(n, generator=g, device="cuda")) / n
+    return hidden, head, t.to(idt), w
+
+
+def run_loss(hidden, head, t, w, scale=1.0, **kw):
+    from recurrent_memory_transformer_diag_b200 import token_loss, token_loss_grad
+    n = hidden.shape[0]
+    loss = torch.full((n,), float("nan"), device="cuda")
+    lse = torch.full((n,), float("nan"), device="cuda")
+    token_loss(hidden, head, t, loss, lse, scale=scale)
+    dh, dw = torch.full_like(hidden, float("nan")), torch.full_like(head, float("nan"))
+    token_loss_grad(hidden, head, t, lse, w, dh, dw, scale=scale, **kw)
+    return loss, lse, dh, dw
+
+
+def check_loss(hidden, head, t, w, scale, got):
+    loss, lse, dh, dw = got
+    dtype, d, v = hidden.dtype, hidden.shape[1], head.shape[0]
+    planes = 3 if dtype == FP else 1
+    L, rl, rloss, A, ok = loss_reference(hidden, head, t, scale)
+    el = logit_error(A, d, planes) + L.abs().max(1).values * U   # and the product with the scale
+    # exponentials and their sum: 2^-22 each, the sum over 128 columns and the tiles; log, the last sums
+    es = (16 + 64 + v / 256) * U
+    check(loss, rloss, 2 * el + es + 4 * U * (rl.abs() + rloss.abs() + 1) + 1e-30, "loss")
+    check(lse, rl, el + es + 4 * U * (rl.abs() + 1) + 1e-30, "lse")
+    assert (loss[~ok] == 0).all() and (lse[~ok] == 0).all()
+    g = torch.where(ok, w.double(), 0.0)[:, None]
+    P = torch.exp(L - rl[:, None]) * g
+    at = t.long().clamp(0, v - 1)[:, None]
+    onehot = torch.zeros_like(P).scatter_add_(1, at, g)
+    H, W = torch.where(ok[:, None], hidden.double(), 0.0), head.double()
+    # P: the logits' and the lse's error, the exponent's product, ex2, the division of the weight,
+    # the subtraction; then three terms or one
+    gap = (L - rl[:, None]).abs()
+    ep = P.abs() * (2 * el + es + 4 * U * (rl.abs() + 1))[:, None] + P.abs() * (gap * 3 + 8) * U + onehot.abs() * 4 * U
+    Q = P - onehot
+    ep = ep + Q.abs() * (2 * U if planes == 3 else half(BF))
+    # an exponential below 2^-126, the smallest normal fp32 number, is flushed to zero: exp(l - lse)
+    # is then off by up to 2^-126 itself, P by that times its weight
+    ep = ep + g.abs() * 2.0 ** -126
+    # products: fp32 operands in chunks of 16 instructions, bf16 over the whole contraction
+    def chain(k):
+        if planes == 3:
+            return (64 + math.ceil(6 * math.ceil(k / 64) / 4) + 16) * U
+        return (k / 16 + 2) * 4 * U
+    want = Q @ W * scale
+    mag = (Q.abs() @ W.abs()) * abs(scale)
+    check(dh, want, (ep @ W.abs()) * abs(scale) + mag * (chain(v) + 24 * U) + want.abs() * half(dtype) + 1e-38, "d_hidden")
+    assert (dh[~ok] == 0).all()
+    want = Q.t() @ H * scale
+    mag = (Q.abs().t() @ H.abs()) * abs(scale)
+    check(dw, want, (ep.t() @ H.abs()) * abs(scale) + mag * (chain(len(t)) + 8 * U) + want.abs() * half(dtype) + 1e-38,
+          "d_head")
+
+
+LOSS = [
+    # n, v, d
+    (1, 1, 8), (1, 300, 64), (2, 255, 72), (3, 256, 64), (5, 257, 136), (127, 512, 256), (128, 1000, 64),
+    (129, 1023, 328), (255, 1025, 64), (257, 777, 512), (300, 5003, 128), (64, 33000, 64), (1030, 259, 2048),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n,v,d", LOSS)
+def test_token_loss_and_gradient(n, v, d, dtype):
+    scale = 1.0 if n % 2 else 0.37
+    hidden, head, t, w = loss_inputs(n + v + d, n, v, d, dtype, torch.int32 if n % 2 else torch.int64,
+                                     0.0 if n < 4 else 0.2)
+    got = run_loss(hidden, head, t, w, scale)
+    check_loss(hidden, head, t, w, scale, got)
+    for a, b in zip(got, run_loss(hidden, head, t, w, scale)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n,v,d,dtype", [
+    (8200, 300, 64, BF),       # two passes over the rows
+    (8192, 17000, 64, BF),     # two pieces of the vocabulary in the gradient, the second ragged
+    (4100, 11003, 64, FP),     # the same for fp32 operands
+])
+def test_token_loss_in_pieces(n, v, d, dtype):
+    hidden, head, t, w = loss_inputs(n, n, v, d, dtype)
+    check_loss(hidden, head, t, w, 1.0, run_loss(hidden, head, t, w))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_token_loss_masked_rows(dtype):
+    """Rows without a target hold NaN and infinities, also in lse and d_loss: they
+    change nothing; targets at and past the vocabulary's end are no targets."""
+    n, v, d = 301, 600, 64
+    hidden, head, t, w = loss_inputs(9, n, v, d, dtype)
+    t[:4] = torch.tensor([-1, v, v + 5, -(1 << 40)], device="cuda")
+    t[-1] = -100
+    off = (t < 0) | (t >= v)
+    clean = run_loss(hidden, head, t, w)
+    dirty, wd = hidden.clone(), w.clone()
+    dirty[off] = float("nan")
+    dirty[off.nonzero()[::2, 0]] = float("inf")
+    wd[off] = float("nan")
+    for a, b in zip(clean, run_loss(dirty, head, t, wd)):
+        assert torch.equal(a, b)
+    check_loss(hidden, head, t, w, 1.0, clean)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_token_loss_no_targets_and_zero_weights(dtype):
+    n, v, d = 70, 300, 64
+    hidden, head, t, w = loss_inputs(3, n, v, d, dtype)
+    loss, lse, dh, dw = run_loss(hidden, head, torch.full_like(t, -1), w)
+    for x in (loss, lse, dh, dw):
+        assert (x == 0).all()
+    loss, lse, dh, dw = run_loss(hidden, head, t, torch.zeros_like(w))
+    assert (loss[t >= 0] > 0).all() and (dh == 0).all() and (dw == 0).all()
+
+
+def test_token_loss_large_logits():
+    """Logits far beyond exp's range, a sure and a hopeless prediction."""
+    n, v, d = 64, 512, 64
+    hidden, head, t, w = loss_inputs(1, n, v, d, BF, ignored=0.0)
+    hidden = (hidden.float() * 300).to(BF)
+    got = run_loss(hidden, head, t, w)
+    assert torch.isfinite(got[0]).all() and float(got[1].max()) > 1000
+    check_loss(hidden, head, t, w, 1.0, got)
+
+
+def test_token_loss_not_a_number():
+    """A NaN in a row with a target shows in that row's loss and gradient only."""
+    n, v, d = 40, 300, 64
+    hidden, head, t, w = loss_inputs(2, n, v, d, FP, ignored=0.0)
+    clean = run_loss(hidden, head, t, w)
+    bad = hidden.clone()
+    bad[7, 3] = float("nan")
+    loss, lse, dh, dw = run_loss(bad, head, t, w)
+    rest = torch.arange(n, device="cuda") != 7
+    assert torch.isnan(loss[7]) and torch.equal(loss[rest], clean[0][rest])
+    assert torch.isnan(dh[7]).all() and torch.equal(dh[rest], clean[2][rest])
+    assert torch.isnan(dw).any()
+
+
+def test_token_loss_weight_range():
+    """Weights of very different and very small size, a negative one, a single one."""
+    n, v, d = 130, 400, 64
+    hidden, head, t, w = loss_inputs(4, n, v, d, FP, ignored=0.0)
+    w = w * torch.logspace(-3, 3, n, device="cuda")
+    w[5] = -w[5]
+    check_loss(hidden, head, t, w, 1.0, run_loss(hidden, head, t, w))
+    w = w * 1e-30
+    got = run_loss(hidden, head, t, w)
+    check_loss(hidden, head, t, w, 1.0, got)
+    one = torch.zeros(n, device="cuda")
+    one[11] = 1.0
+    check_loss(hidden, head, t, one, 1.0, run_loss(hidden, head, t, one))
+
+
+@pytest.mark.parametrize("which", ["hidden", "head"])
+def test_token_loss_one_gradient(which):
+    from recurrent_memory_transformer_diag_b200 import token_loss_grad
+    n, v, d = 200, 900, 128
+    hidden, head, t, w = loss_inputs(6, n, v, d, BF)
+    loss, lse, dh, dw = run_loss(hidden, head, t, w)
+    if which == "hidden":
+        x = torch.empty_like(hidden)
+        token_loss_grad(hidden, head, t, lse, w, d_hidden=x)
+        assert torch.equal(x, dh)
+    else:
+        x = torch.empty_like(head)
+        token_loss_grad(hidden, head, t, lse, w, d_head=x)
+        assert torch.equal(x, dw)
+
+
+def test_token_loss_gradient_against_differences():
+    """Central differences of the loss along a random direction.  The loss along a line
+    is a sum of cumulant functions of a = max |u . w| at most: the third derivative is at
+    most 2 a^3 a row, so the difference is within e^2 / 3 a^3 sum g, plus the losses' own
+    error over e."""
+    from recurrent_memory_transformer_diag_b200 import token_loss
+    n, v, d = 50, 700, 64
+    hidden, head, t, w = loss_inputs(8, n, v, d, FP)
+    loss, lse, dh, dw = run_loss(hidden, head, t, w)
+    g = gen(77)
+    ok = (t >= 0).double()
+
+    def total(h, hd):
+        l, s = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        token_loss(h, hd, t, l, s)
+        return float((l.double() * w.double() * ok).sum())
+
+    e = 2.0 ** -6
+    u = randn(g, n, d)
+    a = float((u.double() @ head.double().t()).abs().max())
+    noise = 64 * U * 20 * float((w.double() * ok).sum()) / e
+    slope = (total(hidden + e * u, head) - total(hidden - e * u, head)) / (2 * e)
+    assert abs(slope - float((dh.double() * u.double()).sum())) <= e * e / 3 * a ** 3 * float((w * ok).sum()) + noise
+    u = randn(g, v, d) / math.sqrt(d)
+    a = float((hidden.double() @ u.double().t()).abs().max())
+    slope = (total(hidden, head + e * u) - total(hidden, head - e * u)) / (2 * e)
+    assert abs(slope - float((dw.double() * u.double()).sum())) <= e * e / 3 * a ** 3 * float((w * ok).sum()) + noise
+
+
+# ------------------------------------------------------------------ streams, graphs, together
+def test_operators_on_another_stream_and_captured():
+    """The whole chain on a side stream, then captured into a graph and replayed on
+    other inputs: the same bits as calls one by one."""
+    from recurrent_memory_transformer_diag_b200 import (embed, embed_grad, rms_norm, rms_norm_grad, token_loss,
+                                                        token_loss_grad)
+    n, v, d = 2500, 700, 128
+    g = gen(12)
+    s = {"table": randn(g, v, d).to(BF), "gain": (1 + 0.1 * randn(g, d)).to(BF),
+         "ids": torch.randint(-1, v, (n,), generator=g, device="cuda"),
+         "t": torch.randint(-1, v, (n,), generator=g, device="cuda"), "w": torch.full((n,), 1.0 / n, device="cuda")}
+
+    def chain(stream=None):
+        x, y = torch.empty(n, d, dtype=BF, device="cuda"), torch.empty(n, d, dtype=BF, device="cuda")
+        r, loss, lse = (torch.empty(n, device="cuda") for _ in range(3))
+        dy, dx, dt, dg = torch.empty_like(x), torch.empty_like(x), torch.empty_like(s["table"]), torch.empty_like(s["gain"])
+        embed(s["ids"], s["table"], x, scale=3.0, stream=stream)
+        rms_norm(x, s["gain"], y, r, stream=stream)
+        token_loss(y, s["table"], s["t"], loss, lse, stream=stream)
+        token_loss_grad(y, s["table"], s["t"], lse, s["w"], dy, dt, stream=stream)
+        rms_norm_grad(x, s["gain"], r, dy, dx, dg, stream=stream)
+        embed_grad(s["ids"], dx, dt, scale=3.0, accumulate=True, stream=stream)
+        return loss, lse, dx, dg, dt
+
+    def same(a, b):
+        torch.cuda.synchronize()
+        return all(torch.equal(x, y) for x, y in zip(a, b))
+
+    want = chain()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = chain(side)
+    assert same(got, want)
+    got = chain(side.cuda_stream)      # a raw handle
+    assert same(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = chain()
+    other = randn(g, v, d).to(BF)
+    s["table"].copy_(other)
+    s["ids"].copy_(torch.randint(-1, v, (n,), generator=g, device="cuda"))
+    want = chain()
+    graph.replay()
+    assert same(held, want)
+    graph.replay()
+    assert same(held, want)
+
+
+def test_two_graphs_with_their_own_workspaces_replayed_side_by_side():
+    from recurrent_memory_transformer_diag_b200 import token_loss, token_loss_grad
+    n, v, d = 300, 2000, 64
+    cases, graphs, outs, want = [], [], [], []
+    for k in range(2):
+        hidden, head, t, w = loss_inputs(20 + k, n, v, d, BF)
+        cases.append((hidden, head, t, w))
+        want.append(run_loss(hidden, head, t, w))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for hidden, head, t, w in cases:
+        loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        dh, dw = torch.empty_like(hidden), torch.empty_like(head)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            token_loss(hidden, head, t, loss, lse)
+            token_loss_grad(hidden, head, t, lse, w, dh, dw)
+        graphs.append(graph)
+        outs.append((loss, lse, dh, dw))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(outs, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_given_workspace_and_status():
+    from recurrent_memory_transformer_diag_b200 import token_loss, workspace_bytes, workspace_status
+    n, v, d = 100, 500, 64
+    hidden, head, t, w = loss_inputs(30, n, v, d, BF)
+    size = workspace_bytes("token_loss", BF, n, d, v)
+    ws = torch.full((size + 512,), 255, dtype=torch.uint8, device="cuda")
+    loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    token_loss(hidden, head, t, loss, lse, workspace=ws[:size])
+    workspace_status(ws)
+    assert (ws[size:] == 255).all()      # nothing behind the size asked for
+    assert torch.equal(loss, run_loss(hidden, head, t, w)[0])
+
+
+@pytest.mark.parametrize("name", ["tiny", "small"])
+def test_score_runs_ids_to_losses(name):
+    """Armt.score: the losses of its embedding, forward, norm and loss, against the
+    64-bit result from the forward's own hidden states; and streamed in two calls."""
+    from recurrent_memory_transformer_diag_b200 import Armt, CONFIGS, make_weights
+    cfg = CONFIGS[name]
+    dt = BF if cfg.dtype == "bf16" else FP
+    S, T, d, v = 4, cfg.seg_len, cfg.d_model, 515
+    g = gen(40)
+    table = randn(g, v, d).to(dt)
+    head = (randn(g, v, d) / math.sqrt(d)).to(dt)
+    gain = (1 + 0.1 * randn(g, d)).to(dt)
+    ids = torch.randint(0, v, (S * T,), generator=g, device="cuda")
+    targets = torch.cat([ids[1:], ids.new_full((1,), -1)])
+    state = lambda: (torch.zeros(cfg.n_layers, d, cfg.phi_dim, device="cuda"),  # noqa: E731
+                     torch.zeros(cfg.n_layers, cfg.phi_dim, device="cuda"))
+    with Armt(cfg, max_segments=S) as m:
+        m.load_weights(make_weights(cfg))
+        A, z = state()
+        loss = torch.empty(S * T, device="cuda")
+        m.score(ids, targets, S, T, table, head, gain, loss, A, z)
+        m.device_status()
+        hidden = torch.empty(S * T, d, dtype=dt, device="cuda")
+        A2, z2 = state()
+        m.forward(table[ids].contiguous(), S, T, hidden, A2, z2)
+        assert torch.equal(A, A2) and torch.equal(z, z2)
+        H = hidden.double()
+        y = (H / (H.square().mean(1, keepdim=True) + cfg.rms_eps).sqrt() * gain.double()).to(dt)
+        _, rl, rloss, Amax, _ = loss_reference(y, head, targets, 1.0)
+        # the norm's own rounding may fall the other way: one step of the type in some elements
+        check(loss, rloss, Amax * (4 * half(dt) + 128 * U) + 1e-4 * U, "score")
+        # two calls of two segments, the state carried
+        A3, z3 = state()
+        parts = []
+        for k in range(2):
+            p = torch.empty(2 * T, device="cuda")
+            sl = slice(k * 2 * T, (k + 1) * 2 * T)
+            m.score(ids[sl], targets[sl], 2, T, table, head, gain, p, A3, z3, carry_state=True)
+            parts.append(p)
+        torch.cuda.synchronize()
+        assert torch.equal(torch.cat(parts), loss)
