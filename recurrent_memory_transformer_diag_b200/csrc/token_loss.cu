@@ -21,9 +21,11 @@
 //
 // Accumulation: tcgen05 adds into fp32 accumulators with truncation, measured
 // here as a relative error of about 2e-6 at K = 2048 growing with K.  Where
-// the result is read in fp32 (the logits; everything of fp32 operands) the
-// accumulator therefore covers `chunk` k-blocks only and the epilogue threads
-// add the chunks in registers, rounded to nearest.
+// the result is read in fp32 (the loss's logits; everything of fp32 operands)
+// the accumulator therefore covers `chunk` k-blocks only and the epilogue
+// threads add the chunks in registers, rounded to nearest.  What is rounded to
+// bf16 right away (P and the gradients of bf16 operands) takes one accumulator
+// over the whole contraction.
 //
 // fp32 operands: x = hi + mid + lo with three bf16 terms (24 bits), and the six
 // products hi lo, lo hi, mid mid, hi mid, mid hi, hi hi run one after another
@@ -50,7 +52,11 @@ constexpr int STAGES = 6;
 constexpr int BOX_BYTES = 64 * BK * 2; // one copied box: 64 x 64 bf16
 constexpr int STAGE_BYTES = 4 * BOX_BYTES;   // two boxes of A, two of B
 constexpr int EPI_WARPS = 8;
-constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
+constexpr int NUM_THREADS = 128 + 32 * EPI_WARPS;   // a control warpgroup and two epilogue ones
+// registers per thread: 384 threads start with 168 (64512 in all); the control
+// warpgroup gives its to the epilogue, which holds 128 sums a thread
+constexpr int CTRL_REGS = 40, EPI_REGS = 232;
+static_assert(128 * CTRL_REGS + 32 * EPI_WARPS * EPI_REGS <= 168 * NUM_THREADS, "register split");
 constexpr int SLOT_BYTES = 4096;       // per epilogue warp: 32 rows x 128 bytes of output
 constexpr int SLOT_OFFSET = STAGES * STAGE_BYTES;
 constexpr int BAR_OFFSET = SLOT_OFFSET + EPI_WARPS * SLOT_BYTES;
@@ -58,7 +64,8 @@ constexpr int SMEM_TOTAL = BAR_OFFSET + 256 + 1024;   // + alignment slack
 static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory per CTA");
 
 constexpr int ROW_GROUP = 32;          // row tiles that share a vocabulary tile before the next one
-constexpr int LOGIT_CHUNK = 4;         // k-blocks per accumulator where the sum is read in fp32
+constexpr int LSE_CHUNK = 8;           // k-blocks per accumulator of the loss's logits (K = 512)
+constexpr int F32_CHUNK = 4;           // ... of everything that fp32 operands give (K = 256)
 constexpr float LOG2E = 1.4426950408889634f;
 
 enum Role { LSE = 0, PROB = 1, GRAD = 2 };
@@ -199,7 +206,7 @@ __device__ __forceinline__ void slot_store(const CUtensorMap* map, uint8_t* slot
 }
 
 // 64 values per lane (a row each) as bf16: columns c0 .. c0+63 of rows c1 .. c1+31.
-__device__ __forceinline__ void emit_bf16x64(const CUtensorMap* map, uint8_t* slot, int lane, const float* v, int c0,
+__device__ __forceinline__ void emit_bf16x64(const CUtensorMap* map, uint8_t* slot, int lane, const float2* v, int c0,
                                              int c1, int c2) {
   slot_free(lane);
 #pragma unroll
@@ -208,7 +215,7 @@ __device__ __forceinline__ void emit_bf16x64(const CUtensorMap* map, uint8_t* sl
     uint32_t* w = reinterpret_cast<uint32_t*>(&pk);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[q * 8 + 2 * i], v[q * 8 + 2 * i + 1]);
+      const __nv_bfloat162 b2 = __float22bfloat162_rn(v[q * 4 + i]);
       w[i] = *reinterpret_cast<const uint32_t*>(&b2);
     }
     *slot_piece(slot, lane, q) = pk;
@@ -216,13 +223,13 @@ __device__ __forceinline__ void emit_bf16x64(const CUtensorMap* map, uint8_t* sl
   slot_store(map, slot, lane, c0, c1, c2, false);
 }
 
-__device__ __forceinline__ void emit_f32x32(const CUtensorMap* map, uint8_t* slot, int lane, const float* v, int c0,
+__device__ __forceinline__ void emit_f32x32(const CUtensorMap* map, uint8_t* slot, int lane, const float2* v, int c0,
                                             int c1, int c2, bool add) {
   slot_free(lane);
 #pragma unroll
   for (int q = 0; q < 8; ++q)
-    *slot_piece(slot, lane, q) = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                                            __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+    *slot_piece(slot, lane, q) = make_uint4(__float_as_uint(v[2 * q].x), __float_as_uint(v[2 * q].y),
+                                            __float_as_uint(v[2 * q + 1].x), __float_as_uint(v[2 * q + 1].y));
   slot_store(map, slot, lane, c0, c1, c2, add);
 }
 
@@ -232,42 +239,52 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Epilogue of one tile: acc holds this thread's row (TMEM lane) of 128
+// Epilogue of one tile: sums holds this thread's row (TMEM lane) of 128
 // columns, those of its half of the tile.
 template <int ROLE>
 __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps& maps, const Job& j, int nv,
-                                            float (&acc)[128], int row_in_tile, int half, int lane, uint8_t* slot) {
+                                            float2 (&sums)[64], int row_in_tile, int half, int lane,
+                                            uint8_t* slot) {
   const int row = j.m0 + row_in_tile;
   const int wrow0 = row - lane;
   const int col0 = j.n0 + half * 128;
   if constexpr (ROLE == LSE) {
+    const float2 scale2 = make_float2(p.scale, p.scale);
 #pragma unroll
-    for (int i = 0; i < 128; ++i) acc[i] *= p.scale;
+    for (int i = 0; i < 64; ++i) sums[i] = __fmul2_rn(sums[i], scale2);
     if (col0 + 128 > p.vocab) {   // the last tile: columns past the vocabulary do not count
 #pragma unroll
-      for (int i = 0; i < 128; ++i)
-        if (col0 + i >= p.vocab) acc[i] = -INFINITY;
+      for (int i = 0; i < 64; ++i) {
+        if (col0 + 2 * i >= p.vocab) sums[i].x = -INFINITY;
+        if (col0 + 2 * i + 1 >= p.vocab) sums[i].y = -INFINITY;
+      }
     }
-    float m = acc[0];
+    float mx[4] = {sums[0].x, sums[0].y, sums[1].x, sums[1].y};
 #pragma unroll
-    for (int i = 1; i < 128; ++i) m = fmaxf(m, acc[i]);
+    for (int i = 2; i < 64; ++i) {
+      mx[2 * (i & 1)] = fmaxf(mx[2 * (i & 1)], sums[i].x);
+      mx[2 * (i & 1) + 1] = fmaxf(mx[2 * (i & 1) + 1], sums[i].y);
+    }
+    const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
     const float ms = m == -INFINITY ? 0.f : m;
-    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+    const float2 neg = make_float2(-ms, -ms), log2e = make_float2(LOG2E, LOG2E);
+    float2 s2[2] = {};
 #pragma unroll
-    for (int i = 0; i < 128; i += 4) {
-      s0 += ex2((acc[i] - ms) * LOG2E);
-      s1 += ex2((acc[i + 1] - ms) * LOG2E);
-      s2 += ex2((acc[i + 2] - ms) * LOG2E);
-      s3 += ex2((acc[i + 3] - ms) * LOG2E);
+    for (int i = 0; i < 64; ++i) {
+      const float2 x = __fmul2_rn(__fadd2_rn(sums[i], neg), log2e);
+      s2[i & 1] = __fadd2_rn(s2[i & 1], make_float2(ex2(x.x), ex2(x.y)));
     }
+    s2[0] = __fadd2_rn(s2[0], s2[1]);
     if (row < nv) {
-      p.part[(long long)(2 * j.ntile + half) * p.part_pitch + row] = make_float2(m, (s0 + s1) + (s2 + s3));
+      p.part[(long long)(2 * j.ntile + half) * p.part_pitch + row] = make_float2(m, s2[0].x + s2[0].y);
       const unsigned at = (unsigned)(p.target[row] - col0);
       if (at < 128u) {
-        float t = acc[0];
+        float t = 0.f;
 #pragma unroll
-        for (int i = 1; i < 128; ++i)
-          if ((unsigned)i == at) t = acc[i];
+        for (int i = 0; i < 64; ++i) {
+          t = at == 2u * i ? sums[i].x : t;
+          t = at == 2u * i + 1 ? sums[i].y : t;
+        }
         p.target_logit[row] = t;
       }
     }
@@ -275,31 +292,38 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
     const bool in = row < nv;
     const float g = in ? p.g[row] : 0.f;
     const float lse = in ? p.lse[row] : 0.f;
+    const float2 scale2 = make_float2(p.scale, p.scale), neg = make_float2(-lse, -lse),
+                 log2e = make_float2(LOG2E, LOG2E), g2 = make_float2(g, g);
 #pragma unroll
-    for (int i = 0; i < 128; ++i) acc[i] = g * ex2((acc[i] * p.scale - lse) * LOG2E);
+    for (int i = 0; i < 64; ++i) {
+      const float2 x = __fmul2_rn(__fadd2_rn(__fmul2_rn(sums[i], scale2), neg), log2e);
+      sums[i] = __fmul2_rn(make_float2(ex2(x.x), ex2(x.y)), g2);
+    }
     if (in) {
       const unsigned at = (unsigned)(p.target[row] - col0);
       if (at < 128u) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i)
-          if ((unsigned)i == at) acc[i] -= g;
+        for (int i = 0; i < 64; ++i) {
+          sums[i].x -= at == 2u * i ? g : 0.f;
+          sums[i].y -= at == 2u * i + 1 ? g : 0.f;
+        }
       }
     }
     if (g == 0.f) {   // rows without a target or weight: zero whatever their logits are
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      for (int i = 0; i < 64; ++i) sums[i] = make_float2(0.f, 0.f);
     }
     const int pc = col0 - p.v0;   // column in the piece
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (wrow0 >= p.n_rows || pc + 64 * h >= p.vc) continue;   // nothing of this box is in P
       for (int t = 0; t < p.planes; ++t) {
-        emit_bf16x64(&maps.out0, slot, lane, acc + 64 * h, pc + 64 * h, wrow0, t);
+        emit_bf16x64(&maps.out0, slot, lane, sums + 32 * h, pc + 64 * h, wrow0, t);
         if (t + 1 < p.planes) {   // what the term just written leaves of the value
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const float r = acc[64 * h + i] - __bfloat162float(__float2bfloat16_rn(acc[64 * h + i]));
-            acc[64 * h + i] = r;
+          for (int i = 0; i < 32; ++i) {
+            const float2 hi = __bfloat1622float2(__float22bfloat162_rn(sums[32 * h + i]));
+            sums[32 * h + i] = make_float2(sums[32 * h + i].x - hi.x, sums[32 * h + i].y - hi.y);
           }
         }
       }
@@ -308,24 +332,25 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
     if (j.dw) {
       if (wrow0 >= p.vc) return;
       const float f = *p.g_max * p.scale;
+      const float2 f2 = make_float2(f, f);
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] *= f;
+      for (int i = 0; i < 64; ++i) sums[i] = __fmul2_rn(sums[i], f2);
       if (p.dw_bf16) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          if (col0 + 64 * h < p.d) emit_bf16x64(&maps.out0, slot, lane, acc + 64 * h, col0 + 64 * h, p.v0 + wrow0, 0);
+          if (col0 + 64 * h < p.d) emit_bf16x64(&maps.out0, slot, lane, sums + 32 * h, col0 + 64 * h, p.v0 + wrow0, 0);
       } else {
 #pragma unroll
         for (int h = 0; h < 4; ++h)
           if (col0 + 32 * h < p.d)
-            emit_f32x32(&maps.out0, slot, lane, acc + 32 * h, col0 + 32 * h, p.v0 + wrow0, 0, false);
+            emit_f32x32(&maps.out0, slot, lane, sums + 16 * h, col0 + 32 * h, p.v0 + wrow0, 0, false);
       }
     } else {
       if (wrow0 >= p.n_rows) return;
 #pragma unroll
       for (int h = 0; h < 4; ++h)
         if (col0 + 32 * h < p.d)
-          emit_f32x32(&maps.out1, slot, lane, acc + 32 * h, col0 + 32 * h, wrow0, j.split, p.dh_add != 0);
+          emit_f32x32(&maps.out1, slot, lane, sums + 16 * h, col0 + 32 * h, wrow0, j.split, p.dh_add != 0);
     }
   }
 }
@@ -340,7 +365,7 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
 //   warp 0      copies: this CTA's 128 rows of A and 128 of the tile's 256 B
 //               rows per stage, counted on the even CTA's barrier
 //   warp 1      (even CTA) issues the products, M = 256, N = 256, K = 16
-//   warps 2..9  epilogue: thread = row, each warp half of the columns
+//   warps 4..11 epilogue: thread = row, each warp half of the columns
 // Two accumulators of 256 TMEM columns: the epilogue of one chunk runs beside
 // the products of the next.  Every wait is bounded (about one second).
 template <int ROLE>
@@ -393,6 +418,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   const int products = p.planes == 3 ? 6 : 1;
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
 
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CTRL_REGS));
   if (skip) {
     // nothing to do
   } else if (warp == 0) {
@@ -489,21 +516,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (global_ns() - t0 > WAIT_LIMIT_NS) break;
       }
     }
+  }   // warps 2 and 3: nothing to do
   } else {
-    // ---------------- epilogue (warps 2..9, both CTAs) ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
+    // ---------------- epilogue (warps 4..11, both CTAs) ----------------
     const int quarter = warp & 3;
-    const int half = (warp - 2) >> 2;
+    const int half = (warp - 4) >> 2;
     const int row_in_tile = (int)rank * 128 + quarter * 32 + lane;
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
-    uint8_t* slot = smem + SLOT_OFFSET + (warp - 2) * SLOT_BYTES;
+    uint8_t* slot = smem + SLOT_OFFSET + (warp - 4) * SLOT_BYTES;
     int buf = 0;
     uint32_t acc_phase = 0;
-    bool ok = true;
+    bool ok = !skip;
     for (int t = cid; t < jobs.total && ok; t += ncl) {
       const Job j = jobs.get(p, nv, t);
-      float acc[128];
+      float2 acc[64];   // this thread's row, 128 columns (pairs: two additions or products an instruction)
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
       const int iters = products * j.kblocks;
       for (int it = 0; it < iters; it += p.chunk) {
         const bool got = mbar_wait_cluster(&tfull[buf], acc_phase, abort_flag);
@@ -520,7 +549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           float v[32];
           tmem_ld32(tbase + (uint32_t)(c * 32), v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[c * 32 + i] += v[i];
+          for (int i = 0; i < 16; ++i) acc[c * 16 + i] = __fadd2_rn(acc[c * 16 + i], make_float2(v[2 * i], v[2 * i + 1]));
         }
         tc_fence_before();
         __syncwarp();
@@ -941,7 +970,7 @@ extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d
     if (e != cudaSuccess) break;
     LossParams p{};
     p.n_rows = nr; p.d = d; p.vocab = vocab; p.planes = L.planes; p.v0 = 0; p.vc = vocab;
-    p.chunk = LOGIT_CHUNK; p.scale = scale; p.n_valid = rp.n_valid; p.target = rp.target;
+    p.chunk = f32 ? F32_CHUNK : LSE_CHUNK; p.scale = scale; p.n_valid = rp.n_valid; p.target = rp.target;
     p.part = (float2*)(ws + L.part); p.part_pitch = nr; p.target_logit = (float*)(ws + L.tlogit); p.err = rp.err;
     e = launch_products<LSE>(maps, p, (long long)div_up(nr, TILE) * div_up(vocab, TILE), st);
     if (e != cudaSuccess) break;
@@ -998,10 +1027,9 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     p.dh_add = v0 > 0;
     e = load_map(&mg.a, ws + L.p, p.vc, pitch, n, L.planes);
     if (e == cudaSuccess) e = make_map(&mp.out0, ws + L.p, false, p.vc, pitch, n, L.planes, 64, 32);
-    p.chunk = LOGIT_CHUNK;
+    p.chunk = f32 ? F32_CHUNK : 1 << 30;
     const int nt = div_up(p.vc, TILE);
     if (e == cudaSuccess) e = launch_products<PROB>(mp, p, (long long)mt * nt, st);
-    p.chunk = f32 ? LOGIT_CHUNK : 1 << 30;   // bf16 results: one accumulator over the whole contraction
     const long long jobs = (p.want_dw ? (long long)nt * dt : 0) + (p.want_dh ? (long long)mt * dt * p.splits : 0);
     if (e == cudaSuccess) e = launch_products<GRAD>(mg, p, jobs, st);
   }
