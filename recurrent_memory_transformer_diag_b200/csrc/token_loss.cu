@@ -82,6 +82,7 @@ struct LossParams {
   float2* part; int part_pitch; float* target_logit;
   // PROB
   const float* lse; const float* g;
+  bf16* p_out; int p_pitch; long long p_plane;   // few rows: P is written without a tensor map
   // GRAD
   int want_dw, want_dh, splits, k_split, dh_add, dw_bf16;
   const float* g_max;
@@ -109,16 +110,20 @@ struct Job {
 
 template <int ROLE>
 struct Jobs {
-  int mt, nt, dt, total, n_dw;
+  int mt, nt, dt, total, n_dw, n_dh;
+  bool dw_first;   // the longer contraction first, so that the shorter tiles fill the end
   __device__ Jobs(const LossParams& p, int nv) {
     mt = (nv + TILE - 1) / TILE;
     nt = (p.vc + TILE - 1) / TILE;
     dt = (p.d + TILE - 1) / TILE;
     if (ROLE == GRAD) {
       n_dw = p.want_dw ? nt * dt : 0;
-      total = n_dw + (p.want_dh ? mt * dt * p.splits : 0);
+      n_dh = p.want_dh ? mt * dt * p.splits : 0;
+      total = n_dw + n_dh;
+      dw_first = nv >= p.k_split;
     } else {
-      n_dw = 0;
+      n_dw = n_dh = 0;
+      dw_first = false;
       total = mt * nt;
     }
   }
@@ -138,14 +143,15 @@ struct Jobs {
       j.n0 = p.v0 + j.ntile * TILE;
       j.ka = j.kb = 0;
       j.kblocks = (p.d + BK - 1) / BK;
-    } else if (t < n_dw) {
+    } else if (dw_first ? t < n_dw : t >= n_dh) {
+      const int r = dw_first ? t : t - n_dh;
       j.dw = true;
-      j.m0 = (t / dt) * TILE;
-      j.n0 = (t % dt) * TILE;
+      j.m0 = (r / dt) * TILE;
+      j.n0 = (r % dt) * TILE;
       j.ka = j.kb = 0;
       j.kblocks = (nv + BK - 1) / BK;
     } else {
-      int r = t - n_dw;
+      int r = dw_first ? t - n_dw : t;
       j.n0 = (r % dt) * TILE;
       r /= dt;
       j.m0 = (r % mt) * TILE;
@@ -571,6 +577,252 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
+// LSE and PROB for few rows (at most NT): bound by reading the head once, so
+// the head is the 128-row operand of one CTA and the hidden rows are the N =
+// NT columns: the shared memory holds almost only head tiles in flight (NT =
+// 64: 9 stages of 16 + 8 KB; NT = 16: 12 stages of 16 + 2 KB, against 96 KB
+// of head per SM in the pair kernel), and the products cost next to nothing.
+// Thread = vocabulary entry; LSE keeps a running (max, sum) per hidden row in
+// registers over all tiles of the CTA and joins the 32 lanes at the end.
+template <int NT>
+struct Few {
+  static constexpr int H_BYTES = NT * 128;
+  static constexpr int STAGE = 2 * BOX_BYTES + H_BYTES;
+  static constexpr int N_STAGES = NT == 16 ? 12 : 9;
+  static constexpr int ROWS = N_STAGES * STAGE;           // lse, g, target of the rows
+  static constexpr int BARS = ROWS + 3 * NT * 4;
+  static constexpr int TOTAL = BARS + 512 + 1024;
+  static constexpr int COLS = 2 * NT < 32 ? 32 : 2 * NT;  // TMEM columns: two accumulators
+  static_assert(TOTAL <= 227 * 1024, "shared memory per CTA");
+};
+constexpr int FEW_THREADS = 256;     // warp 0 copies, warp 1 products, warps 4..7 epilogue
+constexpr int FEW_ROWS = 64;
+
+template <int ROLE, int NT>
+__global__ void __launch_bounds__(FEW_THREADS, 1)
+    token_loss_few_kernel(const __grid_constant__ LossMaps maps, const LossParams p) {
+  using SM = Few<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* s_lse = reinterpret_cast<float*>(smem + SM::ROWS);
+  float* s_g = s_lse + NT;
+  int* s_target = reinterpret_cast<int*>(s_g + NT);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::BARS);
+  uint64_t* empty = full + SM::N_STAGES;
+  uint64_t* tfull = empty + SM::N_STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  __shared__ unsigned skip_cta;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nv = *p.n_valid;
+  if (threadIdx.x == 0) {
+    skip_cta = *reinterpret_cast<volatile unsigned*>(p.err) & ERR_WAIT_TIMEOUT_MASK;
+    for (int s = 0; s < SM::N_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (threadIdx.x < NT) {
+    const bool in = (int)threadIdx.x < nv;
+    s_target[threadIdx.x] = in ? p.target[threadIdx.x] : -1;
+    s_lse[threadIdx.x] = ROLE == PROB && in ? p.lse[threadIdx.x] : 0.f;
+    s_g[threadIdx.x] = ROLE == PROB && in ? p.g[threadIdx.x] : 0.f;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(SM::COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int kblocks = (p.d + BK - 1) / BK;
+  const int products = p.planes == 3 ? 6 : 1;
+  const int iters = products * kblocks;
+  const int tiles = skip_cta || nv == 0 ? 0 : (p.vc + 127) / 128;
+
+  if (warp == 0) {
+    const bool issuer = elect_one();
+    int stage = 0;
+    uint32_t phase = 0, armed = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const int v = p.v0 + t * 128;
+      for (int q = 0; q < products && ok; ++q) {
+        const int ta = products == 1 ? 0 : term_a(q), tb = products == 1 ? 0 : term_b(q);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+          armed &= ~(1u << stage);
+          uint8_t* sa = smem + stage * SM::STAGE;
+          if (issuer) {
+            mbar_expect_tx(&full[stage], SM::STAGE);
+            tma_load_3d(&maps.b, &full[stage], sa, kb * BK, v, tb);
+            tma_load_3d(&maps.b, &full[stage], sa + BOX_BYTES, kb * BK, v + 64, tb);
+            tma_load_3d(&maps.a, &full[stage], sa + 2 * BOX_BYTES, kb * BK, 0, ta);
+          }
+          armed |= 1u << stage;
+          if (++stage == SM::N_STAGES) { stage = 0; phase ^= 1; }
+        }
+      }
+    }
+    if (!ok) {
+      if (issuer) atomicOr(p.err, 1u);
+      *abort_flag = 1;
+    }
+    if (*abort_flag) {   // every issued copy lands before the CTA ends
+      for (int s = 0; s < SM::N_STAGES; ++s) {
+        if (!(armed & (1u << s))) continue;
+        const unsigned long long t0 = global_ns();
+        while (!mbar_try_wait(&full[s], 0) && !mbar_try_wait(&full[s], 1)) {
+          if (global_ns() - t0 > WAIT_LIMIT_NS) break;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    const bool issuer = elect_one();
+    constexpr uint32_t IDESC = idesc_f16(NT, 1, 128);
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      for (int it = 0; it < iters && ok;) {
+        if (!mbar_wait_warp(&tempty[buf], acc_phase ^ 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(buf * NT);
+        const int end = min(iters, it + p.chunk);
+        for (int first = it; it < end; ++it) {
+          if (!mbar_wait_warp(&full[stage], phase, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + stage * SM::STAGE);
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            if (issuer)
+              mma_f16(d_tmem, sw128_desc(sa + kk * 32), sw128_desc(sa + 2 * BOX_BYTES + kk * 32), IDESC,
+                      (it > first || kk > 0) ? 1u : 0u);
+          if (issuer) mma_commit(&empty[stage]);
+          if (++stage == SM::N_STAGES) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        if (issuer) mma_commit(&tfull[buf]);
+        if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+      }
+    }
+    if (!ok) {
+      if (issuer) atomicOr(p.err, 2u);
+      *abort_flag = 1;
+    }
+    if (issuer) mma_commit(drain);   // no product still writes TMEM when it is freed
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try_wait(drain, 0)) {
+      if (global_ns() - t0 > WAIT_LIMIT_NS) break;
+    }
+  } else if (warp >= 4) {
+    const int quarter = warp & 3;
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    float m[ROLE == LSE ? NT : 1], sum[ROLE == LSE ? NT : 1];
+    if constexpr (ROLE == LSE) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        m[i] = -INFINITY;
+        sum[i] = 0.f;
+      }
+    }
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const int v = t * 128 + quarter * 32 + lane;   // in the piece
+      float acc[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[i] = 0.f;
+      for (int it = 0; it < iters; it += p.chunk) {
+        const bool got = mbar_wait(&tfull[buf], acc_phase, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) {
+          if (lane == 0) atomicOr(p.err, 4u);
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * NT);
+#pragma unroll
+        for (int c = 0; c < NT / 16; ++c) {
+          float x[16];
+          tmem_ld16(tbase + (uint32_t)(c * 16), x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[c * 16 + i] += x[i];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[buf]);
+        if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+      }
+      if (!ok) break;
+      const bool in = v < p.vc;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const float l = acc[i] * p.scale;
+        const bool hit = s_target[i] == p.v0 + v;
+        if constexpr (ROLE == LSE) {
+          const float x = in ? l : -INFINITY;
+          const float nm = fmaxf(m[i], x);
+          const float base = nm == -INFINITY ? 0.f : nm;
+          sum[i] = sum[i] * ex2((m[i] - base) * LOG2E) + ex2((x - base) * LOG2E);
+          m[i] = nm;
+          if (hit && in) p.target_logit[i] = l;
+        } else {
+          const float g = s_g[i];
+          float x = g * ex2((l - s_lse[i]) * LOG2E);
+          if (hit) x -= g;
+          if (g == 0.f) x = 0.f;
+          if (in && i < p.n_rows) {
+            bf16* dst = p.p_out + (long long)i * p.p_pitch + v;
+            for (int q = 0; q < p.planes; ++q) {
+              const bf16 y = __float2bfloat16_rn(x);
+              dst[q * p.p_plane] = y;
+              x -= __bfloat162float(y);
+            }
+          }
+        }
+      }
+    }
+    if constexpr (ROLE == LSE) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+          const float om = __shfl_xor_sync(0xffffffffu, m[i], o), os = __shfl_xor_sync(0xffffffffu, sum[i], o);
+          const float nm = fmaxf(m[i], om);
+          const float base = nm == -INFINITY ? 0.f : nm;
+          sum[i] = sum[i] * ex2((m[i] - base) * LOG2E) + os * ex2((om - base) * LOG2E);
+          m[i] = nm;
+        }
+        if (lane == 0 && i < p.part_pitch)
+          p.part[(long long)(blockIdx.x * 4 + quarter) * p.part_pitch + i] = make_float2(m[i], sum[i]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(SM::COLS) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Row order: rows with a target first, in their order; the others fill the
 // end backwards.  Copies the hidden rows there as bf16 (fp32 rows as three
 // terms); rows without a target are written as zeros.
@@ -666,24 +918,35 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
     if (r0 + nr == p.n && lane == 0) *p.n_valid = seen;
   }
   __syncthreads();
-  const int vecs = p.d / 8;   // 8 elements per step
+  const int vecs = p.d / 8;   // 8 elements per step, four steps in flight
   const long long plane = (long long)p.n * p.d;
-  for (int k = threadIdx.x; k < nr * vecs; k += 256) {
-    const int r = k / vecs, c = (k - r * vecs) * 8;
-    const int at = s_slot[r];
-    const bool ok = at >= 0;
-    bf16* dst = p.rows + (long long)(ok ? at : ~at) * p.d + c;
-    if constexpr (sizeof(T) == 2) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (ok) x = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.hidden) + (long long)(r0 + r) * p.d + c);
-      *reinterpret_cast<uint4*>(dst) = x;
-    } else {
-      const float* src = reinterpret_cast<const float*>(p.hidden) + (long long)(r0 + r) * p.d + c;
-      __align__(16) bf16 t[3][8];
+  const T* src = reinterpret_cast<const T*>(p.hidden) + (long long)r0 * p.d;
+  for (int k0 = threadIdx.x; k0 < nr * vecs; k0 += 4 * 256) {
+    Vec8<T> x[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) split3(ok ? src[i] : 0.f, t[0][i], t[1][i], t[2][i]);
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + u * 256;
+      x[u].zero();
+      if (k < nr * vecs && s_slot[k / vecs] >= 0) x[u].load(src + (long long)k * 8);
+    }
 #pragma unroll
-      for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(dst + q * plane) = *reinterpret_cast<uint4*>(t[q]);
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + u * 256;
+      if (k >= nr * vecs) continue;
+      const int r = k / vecs, c = (k - r * vecs) * 8;
+      const int at = s_slot[r] >= 0 ? s_slot[r] : ~s_slot[r];
+      bf16* dst = p.rows + (long long)at * p.d + c;
+      if constexpr (sizeof(T) == 2) {
+        x[u].store(dst);
+      } else {
+        float f[8];
+        x[u].get(f);
+        __align__(16) bf16 t[3][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) split3(f[i], t[0][i], t[1][i], t[2][i]);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(dst + q * plane) = *reinterpret_cast<uint4*>(t[q]);
+      }
     }
   }
 }
@@ -717,8 +980,21 @@ __global__ void __launch_bounds__(1024) join_lse_kernel(const float2* part, int 
     m = nm;
   };
   if (in) {
-#pragma unroll 4
-    for (int i = y; i < n_parts; i += ny) add(part[(long long)i * part_pitch + row]);
+    for (int i0 = y; i0 < n_parts; i0 += 8 * ny) {   // eight at a time: one running maximum for all
+      float2 o[8];
+      float nm = m;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * ny;
+        o[u] = i < n_parts ? part[(long long)i * part_pitch + row] : make_float2(-INFINITY, 0.f);
+        nm = fmaxf(nm, o[u].x);
+      }
+      const float base = nm == -INFINITY ? 0.f : nm;
+      sum *= ex2((m - base) * LOG2E);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) sum += o[u].y * ex2((o[u].x - base) * LOG2E);
+      m = nm;
+    }
   }
   s[threadIdx.x] = make_float2(m, sum);
   __syncthreads();
@@ -794,6 +1070,9 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 int round_up(int a, int b) { return (a + b - 1) / b * b; }
 int div_up(int a, int b) { return (a + b - 1) / b; }
 
+// Blocks of the few-rows kernel: one per SM of the B200, a vocabulary tile of 128 each at least.
+int few_blocks(int v) { return div_up(v, 128) < 148 ? div_up(v, 128) : 148; }
+
 // Workspace of one call, laid out in order.
 struct Layout {
   int planes, rows, pieces, vc, splits, k_split, n_parts;
@@ -801,7 +1080,7 @@ struct Layout {
   Layout(int n, int v, int d, bool f32, bool grad) {
     planes = f32 ? 3 : 1;
     rows = grad ? n : (n < LOSS_ROWS ? n : LOSS_ROWS);
-    n_parts = 2 * div_up(v, TILE);
+    n_parts = n <= FEW_ROWS ? 4 * few_blocks(v) : 2 * div_up(v, TILE);
     vc = v; pieces = 1; splits = k_split = 0;
     if (grad) {
       long long w = P_BYTES / ((long long)n * 2 * planes) / TILE * TILE;
@@ -811,11 +1090,12 @@ struct Layout {
         vc = round_up(div_up(v, pieces), TILE);
         pieces = div_up(v, vc);
       }
-      // dH tiles contract over the piece in splits of about the length of dW's
-      // contraction, so that the tiles of a launch are alike; more and shorter
-      // ones where there are few rows
-      const long long want = 4ll * n;
-      const int ks = (int)(want < 2048 ? 2048 : (want > 8192 ? 8192 : want));
+      // dH tiles contract over the piece in splits, so that a launch has about four
+      // tiles of equal work per CTA pair; of 256 to 8192 columns each
+      const long long mt = div_up(n, TILE), dt = div_up(d, TILE), nt = div_up(vc, TILE);
+      const long long blocks = dt * (mt * div_up(vc, BK) + nt * div_up(n, BK));
+      const long long want = blocks / (4 * 74);
+      const int ks = BK * (int)(want < 4 ? 4 : (want > 128 ? 128 : want));
       splits = div_up(vc, ks);
       k_split = round_up(div_up(vc, splits), BK);
       splits = div_up(vc, k_split);
@@ -892,6 +1172,21 @@ cudaError_t pairs_on_device(int* out) {
   return cudaSuccess;
 }
 
+template <int ROLE, int NT>
+cudaError_t launch_few(const LossMaps& maps, const LossParams& p, cudaStream_t st) {
+  // an attribute of the function on this device; cheap, so set at every launch
+  cudaError_t e = cudaFuncSetAttribute(token_loss_few_kernel<ROLE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Few<NT>::TOTAL);
+  if (e != cudaSuccess) return e;
+  token_loss_few_kernel<ROLE, NT><<<few_blocks(p.vc), FEW_THREADS, Few<NT>::TOTAL, st>>>(maps, p);
+  return cudaGetLastError();
+}
+
+// Hidden rows as the few-rows kernel reads them: boxes of NT rows.
+cudaError_t few_map(CUtensorMap* map, const void* rows, int n, int d, int planes) {
+  return make_map(map, rows, false, d, d, n, planes, BK, n <= 16 ? 16 : FEW_ROWS);
+}
+
 template <int ROLE>
 cudaError_t launch_products(const LossMaps& maps, const LossParams& p, long long jobs, cudaStream_t st) {
   int pairs = 0;
@@ -903,7 +1198,8 @@ cudaError_t launch_products(const LossMaps& maps, const LossParams& p, long long
 }
 
 cudaError_t launch_order_rows(RowParams rp, bool f32, cudaStream_t st) {
-  rp.rows_per_block = rp.n <= 16384 ? 16 : 64;   // blocks scan the targets before them: fewer blocks for many rows
+  // blocks scan the targets before them: few rows each while that is cheap
+  rp.rows_per_block = rp.n <= 2048 ? 4 : (rp.n <= 16384 ? 16 : 64);
   const int grid = div_up(rp.n, rp.rows_per_block);
   if (f32) order_rows_kernel<float><<<grid, 256, 0, st>>>(rp);
   else order_rows_kernel<bf16><<<grid, 256, 0, st>>>(rp);
@@ -966,13 +1262,17 @@ extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d
     rp.n_valid = (int*)(ws + L.n_valid); rp.err = (unsigned*)ws;
     rp.loss_out = loss + r0; rp.lse_out = lse + r0;
     e = launch_order_rows(rp, f32, st);
-    if (e == cudaSuccess) e = load_map(&maps.a, ws + L.rows_b, d, d, nr, L.planes);
+    // up to 64 rows: bound by reading the head (loss_one: 125 us in pairs)
+    const bool few = n <= FEW_ROWS;
+    if (e == cudaSuccess)
+      e = few ? few_map(&maps.a, ws + L.rows_b, nr, d, L.planes) : load_map(&maps.a, ws + L.rows_b, d, d, nr, L.planes);
     if (e != cudaSuccess) break;
     LossParams p{};
     p.n_rows = nr; p.d = d; p.vocab = vocab; p.planes = L.planes; p.v0 = 0; p.vc = vocab;
     p.chunk = f32 ? F32_CHUNK : LSE_CHUNK; p.scale = scale; p.n_valid = rp.n_valid; p.target = rp.target;
     p.part = (float2*)(ws + L.part); p.part_pitch = nr; p.target_logit = (float*)(ws + L.tlogit); p.err = rp.err;
-    e = launch_products<LSE>(maps, p, (long long)div_up(nr, TILE) * div_up(vocab, TILE), st);
+    if (few) e = nr <= 16 ? launch_few<LSE, 16>(maps, p, st) : launch_few<LSE, 64>(maps, p, st);
+    else e = launch_products<LSE>(maps, p, (long long)div_up(nr, TILE) * div_up(vocab, TILE), st);
     if (e != cudaSuccess) break;
     int rb = 32;
     while (rb > 1 && rb / 2 >= nr) rb /= 2;
@@ -1019,6 +1319,8 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
   p.n_rows = n; p.d = d; p.vocab = vocab; p.planes = L.planes; p.scale = scale;
   p.n_valid = rp.n_valid; p.target = rp.target; p.lse = rp.lse; p.g = rp.g; p.g_max = rp.g_max; p.err = rp.err;
   p.want_dw = d_head != nullptr; p.want_dh = d_hidden != nullptr; p.dw_bf16 = !f32; p.k_split = L.k_split;
+  const bool few = n <= FEW_ROWS;
+  if (e == cudaSuccess && few) e = few_map(&mp.a, ws + L.rows_b, n, d, L.planes);
   const int pitch = round_up(L.vc, 64), mt = div_up(n, TILE), dt = div_up(d, TILE);
   for (int v0 = 0; v0 < vocab && e == cudaSuccess; v0 += L.vc) {
     p.v0 = v0;
@@ -1029,7 +1331,12 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     if (e == cudaSuccess) e = make_map(&mp.out0, ws + L.p, false, p.vc, pitch, n, L.planes, 64, 32);
     p.chunk = f32 ? F32_CHUNK : 1 << 30;
     const int nt = div_up(p.vc, TILE);
-    if (e == cudaSuccess) e = launch_products<PROB>(mp, p, (long long)mt * nt, st);
+    p.p_out = (bf16*)(ws + L.p);
+    p.p_pitch = pitch;
+    p.p_plane = (long long)n * pitch;
+    if (e == cudaSuccess)
+      e = !few ? launch_products<PROB>(mp, p, (long long)mt * nt, st)
+               : (n <= 16 ? launch_few<PROB, 16>(mp, p, st) : launch_few<PROB, 64>(mp, p, st));
     const long long jobs = (p.want_dw ? (long long)nt * dt : 0) + (p.want_dh ? (long long)mt * dt * p.splits : 0);
     if (e == cudaSuccess) e = launch_products<GRAD>(mg, p, jobs, st);
   }
