@@ -9,8 +9,9 @@
 //
 //   few tokens: a block owns 32 table rows and looks through all ids; one
 //     launch, nothing to sort.
-//   many tokens: a stable radix sort of (id, n) by 9 bits a pass; then the
-//     sorted list is cut into chunks of 64 tokens, a worker per chunk adds up
+//   many tokens: a stable radix sort of (id, n) by 9 bits a pass (in one block
+//     up to 8192 tokens); then the
+//     sorted list is cut into chunks of 8 to 64 tokens, a worker per chunk adds up
 //     its runs of equal ids and writes those that lie inside it.  Runs that
 //     cross chunks leave one partial sum per chunk, joined in order by a last
 //     kernel, so a token that makes up much of the input is still spread over
@@ -146,6 +147,18 @@ __device__ __forceinline__ int sort_key(const void* ids, int id_bytes, const int
   return id >= 0 && id < vocab ? (int)id : vocab;
 }
 
+// Lanes of the warp with the same digit (RADIX for a lane past the end).
+__device__ __forceinline__ unsigned same_digit(int dg) {
+  unsigned same = 0xffffffffu;
+#pragma unroll
+  for (int b = 0; b <= RADIX_BITS; ++b) {
+    const bool bit = (dg >> b) & 1;
+    const unsigned m = __ballot_sync(0xffffffffu, bit);
+    same &= bit ? m : ~m;
+  }
+  return same;
+}
+
 // Counts of the block's digits: hist[block][digit].
 __global__ void __launch_bounds__(256) sort_count_kernel(const void* ids, int id_bytes, const int* keys, int n,
                                                          int vocab, int shift, int* hist, int* clear) {
@@ -175,12 +188,14 @@ __global__ void __launch_bounds__(256) sort_move_kernel(const void* ids, int id_
   for (int i = threadIdx.x; i < SORT_WARPS * RADIX; i += 256) (&warp_cnt[0][0])[i] = 0;
   // digit totals and the counts of earlier blocks: two digits a thread
   int before[2] = {0, 0}, all[2] = {0, 0};
+#pragma unroll 8
   for (int b = 0; b < (int)gridDim.x; ++b) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = hist[(long long)b * RADIX + 2 * threadIdx.x + k];
-      all[k] += c;
-      if (b < (int)blockIdx.x) before[k] += c;
+    const int2 c = *reinterpret_cast<const int2*>(hist + (long long)b * RADIX + 2 * threadIdx.x);
+    all[0] += c.x;
+    all[1] += c.y;
+    if (b < (int)blockIdx.x) {
+      before[0] += c.x;
+      before[1] += c.y;
     }
   }
   int incl = all[0] + all[1];
@@ -209,7 +224,7 @@ __global__ void __launch_bounds__(256) sort_move_kernel(const void* ids, int id_
   for (int s = 0; s < SORT_STEPS; ++s) {
     const bool in = base + s * 32 + lane < n;
     const int dg = in ? (key[s] >> shift) & (RADIX - 1) : RADIX;   // RADIX: past the end
-    const unsigned same = __match_any_sync(0xffffffffu, dg);
+    const unsigned same = same_digit(dg);
     const int below = __popc(same & ((1u << lane) - 1));
     int old = 0;
     if (in && below == 0) {
@@ -242,8 +257,103 @@ __global__ void __launch_bounds__(256) sort_move_kernel(const void* ids, int id_
   }
 }
 
+// All passes in one block, for up to BLOCK_SORT_MAX tokens: keys in registers,
+// moved through shared memory (one launch instead of two a pass).
+constexpr int BLOCK_SORT_MAX = 8192;
+constexpr int BLOCK_SORT_WARPS = 32;
+constexpr int BLOCK_SORT_STEPS = BLOCK_SORT_MAX / (32 * BLOCK_SORT_WARPS);
+constexpr int BLOCK_SORT_SMEM = 2 * BLOCK_SORT_MAX * 4 + BLOCK_SORT_WARPS * RADIX * 2;
+
+__global__ void __launch_bounds__(1024, 1) sort_block_kernel(const void* ids, int id_bytes, int n, int vocab,
+                                                             int* out_keys, int* out_pos, int* clear) {
+  extern __shared__ int dyn[];
+  __shared__ int s_scan[16];
+  int* s_key = dyn;
+  int* s_pos = dyn + BLOCK_SORT_MAX;
+  unsigned short* cnt = reinterpret_cast<unsigned short*>(dyn + 2 * BLOCK_SORT_MAX);   // [warp][digit]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_warp = (n + 1023) / 1024 * 32;   // keys of a warp, consecutive
+  const int base = warp * per_warp;
+  int key[BLOCK_SORT_STEPS], pos[BLOCK_SORT_STEPS];
+#pragma unroll
+  for (int s = 0; s < BLOCK_SORT_STEPS; ++s) {
+    const int k = s * 32 + lane, i = base + k;
+    pos[s] = i;
+    key[s] = k < per_warp && i < n ? sort_key(ids, id_bytes, nullptr, i, vocab) : -1;
+  }
+  if (threadIdx.x == 0) *clear = 0;
+  for (int shift = 0; shift == 0 || (vocab >> shift) != 0; shift += RADIX_BITS) {
+    for (int i = threadIdx.x; i < BLOCK_SORT_WARPS * RADIX / 2; i += 1024) reinterpret_cast<int*>(cnt)[i] = 0;
+    __syncthreads();
+    int rank[BLOCK_SORT_STEPS];
+#pragma unroll
+    for (int s = 0; s < BLOCK_SORT_STEPS; ++s) {
+      const bool in = key[s] >= 0;
+      const int dg = in ? (key[s] >> shift) & (RADIX - 1) : RADIX;
+      const unsigned same = same_digit(dg);
+      const int below = __popc(same & ((1u << lane) - 1));
+      int old = 0;
+      if (in && below == 0) {
+        old = cnt[warp * RADIX + dg];
+        cnt[warp * RADIX + dg] = (unsigned short)(old + __popc(same));
+      }
+      rank[s] = __shfl_sync(0xffffffffu, old, __ffs(same) - 1) + below;
+      __syncwarp();
+    }
+    __syncthreads();
+    int total = 0, incl = 0;   // a thread per digit: exclusive sums over the warps, then over the digits
+    if (threadIdx.x < RADIX) {
+#pragma unroll 8
+      for (int w = 0; w < BLOCK_SORT_WARPS; ++w) {
+        const int c = cnt[w * RADIX + threadIdx.x];
+        cnt[w * RADIX + threadIdx.x] = (unsigned short)total;
+        total += c;
+      }
+      incl = total;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      if (lane == 31) s_scan[warp] = incl;
+    }
+    __syncthreads();
+    if (threadIdx.x < RADIX) {
+      int start = incl - total;
+      for (int w = 0; w < warp; ++w) start += s_scan[w];
+#pragma unroll 8
+      for (int w = 0; w < BLOCK_SORT_WARPS; ++w) cnt[w * RADIX + threadIdx.x] += (unsigned short)start;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < BLOCK_SORT_STEPS; ++s) {
+      if (key[s] >= 0) {
+        const int at = cnt[warp * RADIX + ((key[s] >> shift) & (RADIX - 1))] + rank[s];
+        s_key[at] = key[s];
+        s_pos[at] = pos[s];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < BLOCK_SORT_STEPS; ++s) {
+      const int k = s * 32 + lane, i = base + k;
+      if (k < per_warp && i < n) {
+        key[s] = s_key[i];
+        pos[s] = s_pos[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < BLOCK_SORT_STEPS; ++s) {
+    if (key[s] >= 0) {
+      out_keys[base + s * 32 + lane] = key[s];
+      out_pos[base + s * 32 + lane] = pos[s];
+    }
+  }
+}
+
 // ---------------------------------------------------------------- sums over the sorted tokens
-constexpr int CHUNK = 64;          // tokens of a worker
+constexpr int CHUNK_MIN = 8, CHUNK_MAX = 64;   // tokens of a worker: fewer where that keeps the device busy
 constexpr int AHEAD = 8;           // rows in flight per thread
 constexpr int FILL_ROWS = 64;      // table rows of a zeroing block
 
@@ -253,6 +363,7 @@ struct SumParams {
   int n, vocab, d;
   int tpw;                 // threads of a worker: a thread owns 8 columns
   int workers;             // per block
+  int chunk;               // tokens of a worker
   int chunks, col_blocks;  // columns in blocks of 8 tpw
   int sum_blocks;          // blocks before the zeroing ones
   float scale;
@@ -293,7 +404,7 @@ __global__ void __launch_bounds__(256) embed_grad_sum_kernel(const SumParams p, 
   const int chunk = (int)(blockIdx.x / p.col_blocks) * p.workers + worker;
   const int col = (cb * p.tpw + t) * 8;
   if (worker >= p.workers || chunk >= p.chunks || col >= p.d) return;
-  const int i0 = chunk * CHUNK, i1 = min(p.n, i0 + CHUNK);
+  const int i0 = chunk * p.chunk, i1 = min(p.n, i0 + p.chunk);
   const int prev = i0 > 0 ? p.keys[i0 - 1] : -1;
   int cur = p.keys[i0];
   bool comes_in = cur == prev;
@@ -343,56 +454,87 @@ __global__ void __launch_bounds__(256) embed_grad_sum_kernel(const SumParams p, 
   finish(i1 < p.n && p.keys[i1] == cur);
 }
 
-// Runs over several chunks: their partial sums in order, 16 groups of chunks
-// side by side, 64 columns a block.
+// Runs over several chunks: their partial sums in order.  A piece of work is
+// 256 columns of a run; a warp does those of a run over up to 32 further
+// chunks by itself, the block shares a longer one (8 groups of chunks side by
+// side).
 template <typename T>
 __global__ void __launch_bounds__(256) embed_grad_join_kernel(const SumParams p, T* d_table) {
-  __shared__ float4 s[256];
-  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;   // 4 columns, group
-  const int col_blocks = (p.d + 63) / 64;
+  __shared__ float s[8][256 + 8];
+  __shared__ int s_long[8];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;   // 8 columns, warp
+  const int col_blocks = (p.d + 255) / 256;
   const long long work = (long long)*p.n_open * col_blocks;
-  for (long long k = blockIdx.x; k < work; k += gridDim.x) {
-    const int2 run = p.open[k / col_blocks];
-    const int col = (int)(k % col_blocks) * 64 + x * 4;
-    // the run's last chunk: the last token with its id
-    int lo = (run.x + 1) * CHUNK, hi = p.n;   // first token behind the run
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (p.keys[mid] <= run.y) lo = mid + 1;
-      else hi = mid;
-    }
-    const int last = (lo - 1) / CHUNK, count = last - run.x;   // chunks after the first
-    const int per = (count + 15) / 16, a = run.x + 1 + y * per, b = min(last + 1, a + per);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (col < p.d) {
-      if (y == 0) acc = *reinterpret_cast<const float4*>(p.part + ((long long)run.x * 2 + 1) * p.d + col);
-#pragma unroll 8
-      for (int c = a; c < b; ++c) {
-        const float4 v = *reinterpret_cast<const float4*>(p.part + (long long)c * 2 * p.d + col);
-        acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+  auto add = [&](float* acc, long long row, int col) {   // one partial sum
+    Vec8<float> v;
+    v.load(p.part + row * p.d + col);
+    float f[8];
+    v.get(f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += f[i];
+  };
+  // a block's eight pieces lie a grid apart: those of one long run go to different blocks
+  for (long long k0 = blockIdx.x; k0 < work; k0 += (long long)gridDim.x * 8) {
+    const long long k = k0 + (long long)y * gridDim.x;
+    bool longer = false;
+    if (k < work) {
+      const int2 run = p.open[k / col_blocks];
+      const int col = (int)(k % col_blocks) * 256 + x * 8;
+      // further chunks that the run reaches: those that begin with its id
+      const long long c = run.x + 1ll + x;
+      const unsigned in = __ballot_sync(0xffffffffu, c < p.chunks && p.keys[c * p.chunk] == run.y);
+      longer = in == 0xffffffffu;
+      const int count = __popc(in);
+      if (!longer && col < p.d) {
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        add(acc, run.x * 2ll + 1, col);
+#pragma unroll 4
+        for (int i = 1; i <= count; ++i) add(acc, (run.x + i) * 2ll, col);
+        write_row(d_table + (long long)run.y * p.d + col, acc, p.scale, p.accumulate != 0);
       }
     }
+    if (x == 0) s_long[y] = longer;
     __syncthreads();
-    s[threadIdx.x] = acc;
-    __syncthreads();
-    if (y == 0 && (x & 1) == 0 && col < p.d) {   // 8 columns a thread
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int g = 0; g < 16; ++g) {
-        const float4 l = s[g * 16 + x], r = s[g * 16 + x + 1];
-        v[0] += l.x; v[1] += l.y; v[2] += l.z; v[3] += l.w;
-        v[4] += r.x; v[5] += r.y; v[6] += r.z; v[7] += r.w;
+    for (int w = 0; w < 8; ++w) {
+      if (!s_long[w]) continue;   // the same for all threads
+      const long long kw = k0 + (long long)w * gridDim.x;
+      const int2 run = p.open[kw / col_blocks];
+      const int col = (int)(kw % col_blocks) * 256 + x * 8;
+      int count = 0;
+      for (int more = 256; more == 256; count += more) {
+        const long long c = run.x + 1ll + count + threadIdx.x;
+        more = __syncthreads_count(c < p.chunks && p.keys[c * p.chunk] == run.y);
       }
-      write_row(d_table + (long long)run.y * p.d + col, v, p.scale, p.accumulate != 0);
+      const int per = (count + 7) / 8, a = run.x + 1 + y * per, b = min(run.x + 1 + count, a + per);
+      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (col < p.d) {
+        if (y == 0) add(acc, run.x * 2ll + 1, col);
+#pragma unroll 4
+        for (int c = a; c < b; ++c) add(acc, c * 2ll, col);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[y][i * 33 + x] = acc[i];
+      __syncthreads();
+      if (y == 0 && col < p.d) {
+        for (int g = 1; g < 8; ++g)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] += s[g][i * 33 + x];
+        write_row(d_table + (long long)run.y * p.d + col, acc, p.scale, p.accumulate != 0);
+      }
+      __syncthreads();
     }
+    __syncthreads();
   }
 }
 
 struct GradLayout {
-  int tiles, chunks;
+  int tiles, chunk, chunks;
   size_t hist, keys[2], pos[2], part, open, n_open, total;
   GradLayout(int n, int d) {
     tiles = (n + SORT_TILE - 1) / SORT_TILE;
-    chunks = (n + CHUNK - 1) / CHUNK;
+    chunk = CHUNK_MIN;
+    while (chunk < CHUNK_MAX && n / chunk > 2048) chunk *= 2;
+    chunks = (n + chunk - 1) / chunk;
     size_t o = 0;
     auto take = [&](size_t bytes) { const size_t at = o; o += (bytes + 255) & ~(size_t)255; return at; };
     n_open = take(4);
@@ -419,21 +561,30 @@ cudaError_t embed_grad(int n, int vocab, int d, const void* ids, int id_bytes, c
   int* hist = (int*)(ws + L.hist);
   int* n_open = (int*)(ws + L.n_open);
   const int *keys = nullptr, *pos = nullptr;
-  int to = 0;
-  for (int shift = 0; shift == 0 || (vocab >> shift) != 0; shift += RADIX_BITS) {   // keys are 0 .. vocab
-    sort_count_kernel<<<L.tiles, 256, 0, st>>>(ids, id_bytes, keys, n, vocab, shift, hist, shift ? nullptr : n_open);
-    int* ok = (int*)(ws + L.keys[to]);
-    int* op = (int*)(ws + L.pos[to]);
-    sort_move_kernel<<<L.tiles, 256, 0, st>>>(ids, id_bytes, keys, pos, n, vocab, shift, hist, ok, op);
-    keys = ok;
-    pos = op;
-    to ^= 1;
+  if (n <= BLOCK_SORT_MAX) {
+    cudaError_t e = cudaFuncSetAttribute(sort_block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BLOCK_SORT_SMEM);
+    if (e != cudaSuccess) return e;
+    keys = (int*)(ws + L.keys[0]);
+    pos = (int*)(ws + L.pos[0]);
+    sort_block_kernel<<<1, 1024, BLOCK_SORT_SMEM, st>>>(ids, id_bytes, n, vocab, (int*)keys, (int*)pos, n_open);
+  } else {
+    int to = 0;
+    for (int shift = 0; shift == 0 || (vocab >> shift) != 0; shift += RADIX_BITS) {   // keys are 0 .. vocab
+      sort_count_kernel<<<L.tiles, 256, 0, st>>>(ids, id_bytes, keys, n, vocab, shift, hist, shift ? nullptr : n_open);
+      int* ok = (int*)(ws + L.keys[to]);
+      int* op = (int*)(ws + L.pos[to]);
+      sort_move_kernel<<<L.tiles, 256, 0, st>>>(ids, id_bytes, keys, pos, n, vocab, shift, hist, ok, op);
+      keys = ok;
+      pos = op;
+      to ^= 1;
+    }
   }
   SumParams p{};
   p.keys = keys; p.pos = pos; p.n = n; p.vocab = vocab; p.d = d;
   const int vecs = d / 8;
   p.tpw = vecs < 256 ? vecs : 256;
   p.workers = 256 / p.tpw;
+  p.chunk = L.chunk;
   p.chunks = L.chunks;
   p.col_blocks = (vecs + p.tpw - 1) / p.tpw;
   p.sum_blocks = (p.chunks + p.workers - 1) / p.workers * p.col_blocks;
@@ -444,7 +595,7 @@ cudaError_t embed_grad(int n, int vocab, int d, const void* ids, int id_bytes, c
   p.n_open = n_open;
   const int fill = accumulate ? 0 : (vocab + FILL_ROWS - 1) / FILL_ROWS;
   embed_grad_sum_kernel<T><<<p.sum_blocks + fill, 256, 0, st>>>(p, d_out, d_table);
-  embed_grad_join_kernel<T><<<148 * 4, 256, 0, st>>>(p, d_table);
+  embed_grad_join_kernel<T><<<148 * 8, 256, 0, st>>>(p, d_table);
   return cudaGetLastError();
 }
 

@@ -5,7 +5,7 @@
 //
 // Bound by memory traffic: every element is read once and written once.  W
 // warps hold a row in registers (a lane VPL groups of 8 columns, at a stride
-// of 256 W columns so that a warp's access is contiguous).  The gradient's
+// of 256 W columns, so that a warp's access is contiguous).  The gradient's
 // blocks walk over the rows with the gain's sums in registers, one partial sum
 // per block, joined in order by a second kernel.
 #include <cmath>
@@ -30,7 +30,6 @@ template <int W>
 __device__ __forceinline__ float row_sum(float x, float* s) {
   x = warp_sum(x);
   if constexpr (W > 1) {
-    __syncthreads();
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
     __syncthreads();
     x = 0.f;
@@ -83,97 +82,101 @@ __global__ void __launch_bounds__(32 * NORM_WARPS) rms_norm_kernel(const T* x, c
   }
 }
 
+// The gradient's block is one row's W warps.  Few columns a lane (two groups of
+// 8 up to 4096 columns) leave room for many blocks, which hide each other's
+// latencies; more warps to a row would spend more instructions on the row's
+// sums than on its elements.  At 32771 x 2048: one warp to a row 104 us, eight
+// 117, four 73 (5.5 TB/s).
+template <typename T, int VPL, int W>
+struct NormGrad {
+  static constexpr int WARPS_PER_SM = VPL * sizeof(T) <= 4 ? 24 : 16;
+  static constexpr int BLOCKS = WARPS_PER_SM / W;
+  static constexpr bool AHEAD = VPL * sizeof(T) <= 8;   // the next row is loaded before this one is worked on
+};
+
 // part[block][d]: sums of dy x r over the block's rows.
 template <typename T, int VPL, int W>
-__global__ void __launch_bounds__(32 * NORM_WARPS) rms_norm_grad_kernel(const T* x, const T* gain, const float* rstd,
-                                                                        const T* dy, T* dx, float* part, int n,
-                                                                        int d) {
-  extern __shared__ float sums[];   // W == 1: [d], the warps' sums joined one warp after another
-  __shared__ float s[NORM_WARPS];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c0 = ((W == 1 ? 0 : warp * 32) + lane) * 8;
-  float acc[VPL][8];
+__global__ void __launch_bounds__(32 * W, NormGrad<T, VPL, W>::BLOCKS)
+    rms_norm_grad_kernel(const T* x, const T* gain, const float* rstd, const T* dy, T* dx, float* part, int n, int d) {
+  constexpr bool AHEAD = NormGrad<T, VPL, W>::AHEAD;
+  __shared__ float s[2][W];   // alternating, so that one barrier a row is enough
+  const int c0 = threadIdx.x * 8;
+  Vec8<T> gv[VPL], xv[VPL], dv[VPL], xn[AHEAD ? VPL : 1], dn[AHEAD ? VPL : 1];
+  float2 acc[VPL][4];
+  float r = 0.f, rn = 0.f;
 #pragma unroll
-  for (int k = 0; k < VPL; ++k)
+  for (int k = 0; k < VPL; ++k) {
+    const int c = c0 + k * 256 * W;
+    gv[k].zero();
+    if (c < d) gv[k].load(gain + c);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[k][i] = 0.f;
-  const int step = W == 1 ? gridDim.x * NORM_WARPS : gridDim.x;
-  for (int row = W == 1 ? blockIdx.x * NORM_WARPS + warp : blockIdx.x; row < n; row += step) {
-    Vec8<T> xv[VPL], dv[VPL];
+    for (int i = 0; i < 4; ++i) acc[k][i] = make_float2(0.f, 0.f);
+  }
+  auto fetch = [&](int row, Vec8<T>* a, Vec8<T>* b, float& rs) {
 #pragma unroll
     for (int k = 0; k < VPL; ++k) {
       const int c = c0 + k * 256 * W;
-      xv[k].zero();
-      dv[k].zero();
-      if (c < d) {
-        xv[k].load(x + (long long)row * d + c);
-        dv[k].load(dy + (long long)row * d + c);
+      a[k].zero();
+      b[k].zero();
+      if (row < n && c < d) {
+        a[k].load(x + (long long)row * d + c);
+        b[k].load(dy + (long long)row * d + c);
       }
     }
-    const float r = rstd[row];
-    float ux = 0.f;
+    rs = row < n ? rstd[row] : 0.f;
+  };
+  int row = blockIdx.x, turn = 0;
+  if constexpr (AHEAD) fetch(row, xn, dn, rn);
+  for (; row < n; row += gridDim.x, turn ^= 1) {
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int k = 0; k < VPL; ++k) {
+        xv[k] = xn[k];
+        dv[k] = dn[k];
+      }
+      r = rn;
+      fetch(row + (int)gridDim.x, xn, dn, rn);
+    } else {
+      fetch(row, xv, dv, r);
+    }
+    float2 ux = make_float2(0.f, 0.f);
+    const float2 r2 = make_float2(r, r);
 #pragma unroll
     for (int k = 0; k < VPL; ++k) {
-      const int c = c0 + k * 256 * W;
-      if (c < d) {
-        Vec8<T> gv;
-        gv.load(gain + c);
-        float a[8], b[8], g[8];
-        xv[k].get(a);
-        dv[k].get(b);
-        gv.get(g);
+      float2 a[4], b[4], g[4];
+      xv[k].get(&a[0].x);
+      dv[k].get(&b[0].x);
+      gv[k].get(&g[0].x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ux = fmaf(b[i] * g[i], a[i], ux);
-          acc[k][i] = fmaf(b[i] * a[i], r, acc[k][i]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        ux = __ffma2_rn(__fmul2_rn(b[i], g[i]), a[i], ux);
+        acc[k][i] = __ffma2_rn(__fmul2_rn(b[i], a[i]), r2, acc[k][i]);
       }
     }
-    const float m = row_sum<W>(ux, s) / (float)d * r * r;
+    const float m = -row_sum<W>(ux.x + ux.y, s[turn]) / (float)d * r * r;
+    const float2 m2 = make_float2(m, m);
 #pragma unroll
     for (int k = 0; k < VPL; ++k) {
       const int c = c0 + k * 256 * W;
       if (c < d) {
-        Vec8<T> gv;
-        gv.load(gain + c);
-        float a[8], b[8], g[8];
-        xv[k].get(a);
-        dv[k].get(b);
-        gv.get(g);
+        float2 a[4], b[4], g[4];
+        xv[k].get(&a[0].x);
+        dv[k].get(&b[0].x);
+        gv[k].get(&g[0].x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = r * (b[i] * g[i] - a[i] * m);
-        xv[k].set(a);
+        for (int i = 0; i < 4; ++i) a[i] = __fmul2_rn(__ffma2_rn(a[i], m2, __fmul2_rn(b[i], g[i])), r2);
+        xv[k].set(&a[0].x);
         xv[k].store(dx + (long long)row * d + c);
       }
     }
   }
-  float* out = part + (long long)blockIdx.x * d;
-  if constexpr (W == 1) {
-    for (int w = 0; w < NORM_WARPS; ++w) {
-      if (warp == w) {
 #pragma unroll
-        for (int k = 0; k < VPL; ++k) {
-          const int c = c0 + k * 256;
-          if (c < d) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int at = i * (d / 8) + c / 8;   // lanes on consecutive words
-              sums[at] = (w ? sums[at] : 0.f) + acc[k][i];
-            }
-          }
-        }
-      }
-      __syncthreads();
-    }
-    for (int c = threadIdx.x; c < d; c += 32 * NORM_WARPS) out[c] = sums[(c & 7) * (d / 8) + c / 8];
-  } else {
-#pragma unroll
-    for (int k = 0; k < VPL; ++k) {
-      const int c = c0 + k * 256 * W;
-      if (c < d) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) out[c + i] = acc[k][i];
-      }
+  for (int k = 0; k < VPL; ++k) {
+    const int c = c0 + k * 256 * W;
+    if (c < d) {
+      float4* out = reinterpret_cast<float4*>(part + (long long)blockIdx.x * d + c);
+      out[0] = make_float4(acc[k][0].x, acc[k][0].y, acc[k][1].x, acc[k][1].y);
+      out[1] = make_float4(acc[k][2].x, acc[k][2].y, acc[k][3].x, acc[k][3].y);
     }
   }
 }
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(1024) rms_norm_gain_kernel(const float* part, 
   const int per = (parts + 31) / 32;
   float acc = 0.f;
   if (c < d) {
-#pragma unroll 4
+#pragma unroll 8
     for (int k = y * per; k < min(parts, (y + 1) * per); ++k) acc += part[(long long)k * d + c];
   }
   s[y][x] = acc;
@@ -197,27 +200,40 @@ __global__ void __launch_bounds__(1024) rms_norm_gain_kernel(const float* part, 
   }
 }
 
-constexpr int NORM_WARP_D = 2048;                  // widest row of one warp
+constexpr int NORM_WARP_D = 2048;                  // widest row that one warp normalises
 constexpr int NORM_MAX_D = 256 * 8 * NORM_WARPS;   // 8 groups a lane, 8 warps a row
 
-int grad_blocks(int n, int d) {
-  const int rows = d <= NORM_WARP_D ? NORM_WARPS : 1;   // per block and step
-  const int want = (n + rows - 1) / rows;
-  return want < 2 * 148 ? want : 2 * 148;
+// Blocks of the gradient: what one wave of the B200's 148 SMs holds.
+template <typename T, int VPL, int W>
+int grad_blocks(int n) {
+  constexpr int most = 148 * NormGrad<T, VPL, W>::BLOCKS;
+  return n < most ? n : most;
 }
 
-// W = 1 up to 2048 columns: no block-wide sums; above, the block holds a row
-// (16 groups a lane would spill the gradient's registers).
-#define ARMT_NORM_CASES(F) \
-  if (d <= 256) { F(1, 1) } else if (d <= 512) { F(2, 1) } else if (d <= 1024) { F(4, 1) } \
-  else if (d <= NORM_WARP_D) { F(8, 1) } else if (d <= 4096) { F(2, NORM_WARPS) } \
-  else if (d <= 8192) { F(4, NORM_WARPS) } else { F(8, NORM_WARPS) }
+// By the row's length: two groups of 8 a lane as far as 8 warps reach.
+#define ARMT_NORM_GRAD_CASES(F) \
+  if (d <= 256) { F(1, 1) } else if (d <= 512) { F(2, 1) } else if (d <= 1024) { F(2, 2) } \
+  else if (d <= 2048) { F(2, 4) } else if (d <= 4096) { F(2, 8) } else if (d <= 8192) { F(4, 8) } else { F(4, 16) }
+
+template <typename T>
+int grad_parts(int n, int d) {
+#define ARMT_F(V, W) return grad_blocks<T, V, W>(n);
+  ARMT_NORM_GRAD_CASES(ARMT_F)
+#undef ARMT_F
+}
 
 template <typename T>
 cudaError_t norm(const T* x, const T* gain, T* y, float* rstd, int n, int d, float eps, cudaStream_t st) {
+  // one warp to a row: no block-wide sums; above, the block holds a row
   const int grid = d <= NORM_WARP_D ? (n + NORM_WARPS - 1) / NORM_WARPS : n;
 #define ARMT_F(V, W) rms_norm_kernel<T, V, W><<<grid, 32 * NORM_WARPS, 0, st>>>(x, gain, y, rstd, n, d, eps);
-  ARMT_NORM_CASES(ARMT_F)
+  if (d <= 256) { ARMT_F(1, 1) }
+  else if (d <= 512) { ARMT_F(2, 1) }
+  else if (d <= 1024) { ARMT_F(4, 1) }
+  else if (d <= NORM_WARP_D) { ARMT_F(8, 1) }
+  else if (d <= 4096) { ARMT_F(2, NORM_WARPS) }
+  else if (d <= 8192) { ARMT_F(4, NORM_WARPS) }
+  else { ARMT_F(8, NORM_WARPS) }
 #undef ARMT_F
   return cudaGetLastError();
 }
@@ -225,11 +241,9 @@ cudaError_t norm(const T* x, const T* gain, T* y, float* rstd, int n, int d, flo
 template <typename T>
 cudaError_t norm_grad(const T* x, const T* gain, const float* rstd, const T* dy, T* dx, T* d_gain, float* part, int n,
                       int d, cudaStream_t st) {
-  const int grid = grad_blocks(n, d);
-  const size_t smem = d <= NORM_WARP_D ? (size_t)d * 4 : 0;
-#define ARMT_F(V, W) \
-  rms_norm_grad_kernel<T, V, W><<<grid, 32 * NORM_WARPS, smem, st>>>(x, gain, rstd, dy, dx, part, n, d);
-  ARMT_NORM_CASES(ARMT_F)
+  const int grid = grad_parts<T>(n, d);
+#define ARMT_F(V, W) rms_norm_grad_kernel<T, V, W><<<grid, 32 * W, 0, st>>>(x, gain, rstd, dy, dx, part, n, d);
+  ARMT_NORM_GRAD_CASES(ARMT_F)
 #undef ARMT_F
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -265,7 +279,7 @@ extern "C" armt_status armt_rms_norm_grad_workspace(armt_dtype dtype, int n, int
   *bytes = 0;
   const armt_status s = check_norm(dtype, n, d);
   if (s != ARMT_OK) return s;
-  *bytes = (size_t)grad_blocks(n, d) * d * 4;
+  *bytes = (size_t)(dtype == ARMT_BF16 ? grad_parts<bf16>(n, d) : grad_parts<float>(n, d)) * d * 4;
   return ARMT_OK;
 }
 

@@ -11,7 +11,6 @@ unless the caller passes one (a uint8 tensor of ``workspace_bytes`` bytes).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional
 
@@ -66,40 +65,44 @@ def _ids(where: str, name: str, t, n: Optional[int], device) -> int:
     return _ID_BYTES[t.dtype]
 
 
-def _overlap(a, b) -> bool:
-    return (a is not None and b is not None and a.data_ptr() < b.data_ptr() + b.numel() * b.element_size()
-            and b.data_ptr() < a.data_ptr() + a.numel() * a.element_size())
-
-
 def _apart(where: str, outputs, others):
     """No output shares memory with an input or another output."""
-    for i, (name, t) in enumerate(outputs):
-        for other, u in list(others) + outputs[:i]:
-            if _overlap(t, u):
+    spans = [(name, t.data_ptr(), t.nbytes) for name, t in others if t is not None]
+    for name, t in outputs:
+        a, size = t.data_ptr(), t.nbytes
+        for other, b, n in spans:
+            if a < b + n and b < a + size:
                 _bad(where, f"{name} overlaps {other}")
+        spans.append((name, a, size))
 
 
-@contextlib.contextmanager
+class _Here:
+    """The current device and stream as they are."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
 def on_stream(stream, device):
     """Make `device` and `stream` (a PyTorch stream, a raw handle, or None for the
     device's current one) current, so that what is allocated inside belongs to it."""
     if stream is None:
-        if torch.cuda.current_device() == device.index:
-            yield
-        else:
-            with torch.cuda.device(device):
-                yield
-        return
+        return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     if stream.device != device:
         _bad("stream", f"the stream belongs to {stream.device}, the tensors to {device}")
-    with torch.cuda.stream(stream):
-        yield
+    return torch.cuda.stream(stream)
 
 
-def _handle() -> int:
-    return torch.cuda.current_stream().cuda_stream
+def _handle(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _space(where: str, size_fn: str, args, workspace, device):
@@ -142,7 +145,7 @@ def workspace_status(workspace, stream=None):
     """Wait for the stream; raises if a bounded wait ran out in the last
     ``token_loss`` or ``token_loss_grad`` call that used this workspace."""
     with on_stream(stream, workspace.device):
-        _check(lib().armt_workspace_status(workspace.data_ptr(), _handle()), "armt_workspace_status")
+        _check(lib().armt_workspace_status(workspace.data_ptr(), _handle(workspace.device)), "armt_workspace_status")
 
 
 def embed(ids, table, out, scale: float = 1.0, stream=None):
@@ -155,7 +158,7 @@ def embed(ids, table, out, scale: float = 1.0, stream=None):
     _apart(w, [("out", out)], [("table", table), ("ids", ids)])
     with on_stream(stream, dev):
         _check(lib().armt_embed(t, n, vocab, d, ids.data_ptr(), b, table.data_ptr(), scale, out.data_ptr(),
-                                _handle()), w)
+                                _handle(dev)), w)
 
 
 def embed_grad(ids, d_out, d_table, scale: float = 1.0, accumulate: bool = False, workspace=None, stream=None):
@@ -172,7 +175,7 @@ def embed_grad(ids, d_out, d_table, scale: float = 1.0, accumulate: bool = False
     with on_stream(stream, dev):
         at, size, keep = _space(w, "armt_embed_grad_workspace", (t, n, vocab, d), workspace, dev)
         _check(lib().armt_embed_grad(t, n, vocab, d, ids.data_ptr(), b, d_out.data_ptr(), scale, d_table.data_ptr(),
-                                     int(bool(accumulate)), at, size, _handle()), w)
+                                     int(bool(accumulate)), at, size, _handle(dev)), w)
 
 
 def rms_norm(x, gain, y, rstd=None, eps: float = 1e-5, stream=None):
@@ -188,7 +191,7 @@ def rms_norm(x, gain, y, rstd=None, eps: float = 1e-5, stream=None):
         _apart(w, [("rstd", rstd)], [("x", x), ("gain", gain), ("y", y)])
     with on_stream(stream, dev):
         _check(lib().armt_rms_norm(t, n, d, x.data_ptr(), gain.data_ptr(), eps, y.data_ptr(),
-                                   None if rstd is None else rstd.data_ptr(), _handle()), w)
+                                   None if rstd is None else rstd.data_ptr(), _handle(dev)), w)
 
 
 def rms_norm_grad(x, gain, rstd, dy, dx, d_gain, workspace=None, stream=None):
@@ -207,7 +210,7 @@ def rms_norm_grad(x, gain, rstd, dy, dx, d_gain, workspace=None, stream=None):
     with on_stream(stream, dev):
         at, size, keep = _space(w, "armt_rms_norm_grad_workspace", (t, n, d), workspace, dev)
         _check(lib().armt_rms_norm_grad(t, n, d, x.data_ptr(), gain.data_ptr(), rstd.data_ptr(), dy.data_ptr(),
-                                        dx.data_ptr(), d_gain.data_ptr(), at, size, _handle()), w)
+                                        dx.data_ptr(), d_gain.data_ptr(), at, size, _handle(dev)), w)
 
 
 def _loss_args(w, hidden, head, targets):
@@ -231,7 +234,7 @@ def token_loss(hidden, head, targets, loss, lse, scale: float = 1.0, workspace=N
     with on_stream(stream, dev):
         at, size, keep = _space(w, "armt_token_loss_workspace", (t, n, vocab, d, 0), workspace, dev)
         _check(lib().armt_token_loss(t, n, vocab, d, hidden.data_ptr(), head.data_ptr(), targets.data_ptr(), b, scale,
-                                     loss.data_ptr(), lse.data_ptr(), at, size, _handle()), w)
+                                     loss.data_ptr(), lse.data_ptr(), at, size, _handle(dev)), w)
 
 
 def token_loss_grad(hidden, head, targets, lse, d_loss, d_hidden=None, d_head=None, scale: float = 1.0,
@@ -258,4 +261,4 @@ def token_loss_grad(hidden, head, targets, lse, d_loss, d_hidden=None, d_head=No
         _check(lib().armt_token_loss_grad(t, n, vocab, d, hidden.data_ptr(), head.data_ptr(), targets.data_ptr(), b,
                                           scale, lse.data_ptr(), d_loss.data_ptr(),
                                           None if d_hidden is None else d_hidden.data_ptr(),
-                                          None if d_head is None else d_head.data_ptr(), at, size, _handle()), w)
+                                          None if d_head is None else d_head.data_ptr(), at, size, _handle(dev)), w)

@@ -75,7 +75,8 @@ EMBED_GRAD = [
     (5000, 511, 64, "uniform"), (5000, 512, 64, "uniform"), (5000, 262145, 8, "uniform"),   # 1, 2, 3 passes
     (20011, 3001, 256, "skewed"), (9000, 100, 2048, "one"), (6400, 100, 64, "blocks"),
     (4097, 77, 2056, "skewed"),            # columns in two blocks
-    (3000, 50, 16, "none"),
+    (3000, 50, 16, "none"), (8192, 300, 64, "skewed"), (8193, 300, 64, "skewed"), (12000, 511, 64, "uniform"),
+    (12000, 512, 64, "uniform"), (12000, 262145, 8, "uniform"), (9000, 5, 64, "none"),
 ]
 
 
