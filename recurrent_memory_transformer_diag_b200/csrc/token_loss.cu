@@ -65,6 +65,7 @@ static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory per CTA");
 
 constexpr int ROW_GROUP = 32;          // row tiles that share a vocabulary tile before the next one
 constexpr int LSE_CHUNK = 8;           // k-blocks per accumulator of the loss's logits (K = 512)
+constexpr int FEW_CHUNK = 2;           // ... of few rows' logits, where it costs nothing (K = 128)
 constexpr int F32_CHUNK = 4;           // ... of everything that fp32 operands give (K = 256)
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -73,6 +74,7 @@ enum Role { LSE = 0, PROB = 1, GRAD = 2 };
 struct LossParams {
   int n_rows, d, vocab;
   int planes;                 // 1: bf16 operands; 3: fp32 operands as three bf16 terms
+  int p_planes;               // terms of P: 1 or 2 beside bf16 operands, 3 beside fp32 ones
   int v0, vc;                 // vocabulary piece
   int chunk;                  // k-blocks per accumulator
   float scale;
@@ -83,6 +85,8 @@ struct LossParams {
   // PROB
   const float* lse; const float* g;
   bf16* p_out; int p_pitch; long long p_plane;   // few rows: P is written without a tensor map
+  // few rows, LSE: rows in their own order, targets as the caller gave them
+  const void* ids; int id_bytes; unsigned* block_err;
   // GRAD
   int want_dw, want_dh, splits, k_split, dh_add, dw_bf16;
   const float* g_max;
@@ -94,15 +98,23 @@ struct LossMaps {
   CUtensorMap out0, out1;     // PROB: P; GRAD: dW, dH partial sums
 };
 
-// Terms multiplied in product q of fp32 operands (smallest products first).
-__device__ __forceinline__ int term_a(int q) { return (0x021010 >> (4 * (5 - q))) & 15; }
-__device__ __forceinline__ int term_b(int q) { return (0x201100 >> (4 * (5 - q))) & 15; }
+// Products of a tile and the terms that product q multiplies (smallest products
+// first): six with fp32 operands; with bf16 ones as many as the first operand
+// (P) has terms.
+__device__ __forceinline__ int n_products(int planes, int a_terms) { return planes == 3 ? 6 : a_terms; }
+__device__ __forceinline__ int term_a(int q, int products) {
+  return products == 6 ? (0x021010 >> (4 * (5 - q))) & 15 : products - 1 - q;
+}
+__device__ __forceinline__ int term_b(int q, int products) {
+  return products == 6 ? (0x201100 >> (4 * (5 - q))) & 15 : 0;
+}
 
 // One tile of work: D[256 x 256] = A B^T over k-blocks kb = 0 .. kblocks-1.
 struct Job {
   int m0, n0;        // first row / column in the operands' own coordinates
   int ka, kb;        // first k coordinate in A / B
   int kblocks;
+  int n;             // columns computed: 256, or 128 where the gradient's width ends there
   bool dw;           // GRAD: a tile of dW (A is P transposed)
   int split;         // GRAD, dH: which partial sum
   int ntile;         // LSE: index of the vocabulary tile
@@ -132,6 +144,7 @@ struct Jobs {
     j.dw = false;
     j.split = 0;
     j.ntile = 0;
+    j.n = TILE;
     if (ROLE != GRAD) {
       // consecutive tiles share a vocabulary tile: the head is read from HBM
       // once per group of rows, the group's hidden rows stay in L2
@@ -160,6 +173,7 @@ struct Jobs {
       j.kb = p.v0 + j.ka;
       j.kblocks = (min(p.vc - j.ka, p.k_split) + BK - 1) / BK;
     }
+    if (ROLE == GRAD && p.d - j.n0 <= TILE / 2) j.n = TILE / 2;
     return j;
   }
 };
@@ -323,9 +337,9 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (wrow0 >= p.n_rows || pc + 64 * h >= p.vc) continue;   // nothing of this box is in P
-      for (int t = 0; t < p.planes; ++t) {
+      for (int t = 0; t < p.p_planes; ++t) {
         emit_bf16x64(&maps.out0, slot, lane, sums + 32 * h, pc + 64 * h, wrow0, t);
-        if (t + 1 < p.planes) {   // what the term just written leaves of the value
+        if (t + 1 < p.p_planes) {   // what the term just written leaves of the value
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float2 hi = __bfloat1622float2(__float22bfloat162_rn(sums[32 * h + i]));
@@ -421,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 
   const int nv = *p.n_valid;
   const Jobs<ROLE> jobs(p, nv);
-  const int products = p.planes == 3 ? 6 : 1;
+  const int products = n_products(p.planes, ROLE == GRAD ? p.p_planes : 1);
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
 
   if (warp < 4) {
@@ -440,22 +454,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const bool a_mn = ROLE == GRAD && j.dw, b_mn = ROLE == GRAD;
       const CUtensorMap* ma = &maps.a;
       const CUtensorMap* mb = ROLE == GRAD && j.dw ? &maps.c : &maps.b;
-      const int am = j.m0 + (int)rank * 128, bn = j.n0 + (int)rank * 128;
+      const int am = j.m0 + (int)rank * 128, bn = j.n0 + (int)rank * (j.n / 2);
       for (int q = 0; q < products && ok; ++q) {
-        const int ta = products == 1 ? 0 : term_a(q), tb = products == 1 ? 0 : term_b(q);
+        const int ta = term_a(q, products), tb = term_b(q, products);
         for (int kb = 0; kb < j.kblocks; ++kb) {
           if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
           armed &= ~(1u << stage);
           uint8_t* sa = smem + stage * STAGE_BYTES;
           if (issuer) {
-            if (leader) mbar_expect_tx(&full[stage], 2 * STAGE_BYTES);   // both CTAs' copies
+            // both CTAs' copies
+            if (leader) mbar_expect_tx(&full[stage], 2 * (2 * BOX_BYTES + j.n / 128 * BOX_BYTES));
             const uint32_t fb = full0 + (uint32_t)(stage * sizeof(uint64_t));
             const int ka = j.ka + kb * BK, kbb = j.kb + kb * BK;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               tma_load_3d_pair(ma, fb, sa + h * BOX_BYTES, a_mn ? am + 64 * h : ka, a_mn ? ka : am + 64 * h, ta);
-              tma_load_3d_pair(mb, fb, sa + (2 + h) * BOX_BYTES, b_mn ? bn + 64 * h : kbb, b_mn ? kbb : bn + 64 * h,
-                               tb);
+              if (128 * h < j.n)
+                tma_load_3d_pair(mb, fb, sa + (2 + h) * BOX_BYTES, b_mn ? bn + 64 * h : kbb, b_mn ? kbb : bn + 64 * h,
+                                 tb);
             }
           }
           armed |= 1u << stage;
@@ -486,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       for (int t = cid; t < jobs.total && ok; t += ncl) {
         const Job j = jobs.get(p, nv, t);
         const bool a_mn = ROLE == GRAD && j.dw, b_mn = ROLE == GRAD;
-        const uint32_t idesc = idesc_f16(TILE, 1, TILE) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+        const uint32_t idesc = idesc_f16(j.n, 1, TILE) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
         const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
         const int iters = products * j.kblocks;
         for (int it = 0; it < iters && ok;) {
@@ -584,6 +600,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 // of head per SM in the pair kernel), and the products cost next to nothing.
 // Thread = vocabulary entry; LSE keeps a running (max, sum) per hidden row in
 // registers over all tiles of the CTA and joins the 32 lanes at the end.
+// A row's target, -1 where it has none.
+__device__ __forceinline__ int target_of(const void* ids, int id_bytes, int i, int vocab) {
+  const long long t = load_id(ids, id_bytes, i);
+  return t >= 0 && t < vocab ? (int)t : -1;
+}
+
 template <int NT>
 struct Few {
   static constexpr int H_BYTES = NT * 128;
@@ -617,9 +639,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   __shared__ unsigned skip_cta;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nv = *p.n_valid;
+  const bool own_order = ROLE == LSE && p.ids != nullptr;
+  const int nv = own_order ? p.n_rows : *p.n_valid;
+  __shared__ unsigned s_err;
+  unsigned* const err = own_order ? &s_err : p.err;   // own_order: the first kernel of the call, nothing is cleared yet
   if (threadIdx.x == 0) {
-    skip_cta = *reinterpret_cast<volatile unsigned*>(p.err) & ERR_WAIT_TIMEOUT_MASK;
+    s_err = 0;
+    skip_cta = own_order ? 0 : *reinterpret_cast<volatile unsigned*>(p.err) & ERR_WAIT_TIMEOUT_MASK;
     for (int s = 0; s < SM::N_STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -634,7 +660,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   }
   if (threadIdx.x < NT) {
     const bool in = (int)threadIdx.x < nv;
-    s_target[threadIdx.x] = in ? p.target[threadIdx.x] : -1;
+    s_target[threadIdx.x] = !in ? -1 : (own_order ? target_of(p.ids, p.id_bytes, threadIdx.x, p.vocab) : p.target[threadIdx.x]);
     s_lse[threadIdx.x] = ROLE == PROB && in ? p.lse[threadIdx.x] : 0.f;
     s_g[threadIdx.x] = ROLE == PROB && in ? p.g[threadIdx.x] : 0.f;
   }
@@ -649,7 +675,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int kblocks = (p.d + BK - 1) / BK;
-  const int products = p.planes == 3 ? 6 : 1;
+  const int products = n_products(p.planes, 1);
   const int iters = products * kblocks;
   const int tiles = skip_cta || nv == 0 ? 0 : (p.vc + 127) / 128;
 
@@ -661,7 +687,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const int v = p.v0 + t * 128;
       for (int q = 0; q < products && ok; ++q) {
-        const int ta = products == 1 ? 0 : term_a(q), tb = products == 1 ? 0 : term_b(q);
+        const int ta = term_a(q, products), tb = term_b(q, products);
         for (int kb = 0; kb < kblocks; ++kb) {
           if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
           armed &= ~(1u << stage);
@@ -678,7 +704,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       }
     }
     if (!ok) {
-      if (issuer) atomicOr(p.err, 1u);
+      if (issuer) atomicOr(err, 1u);
       *abort_flag = 1;
     }
     if (*abort_flag) {   // every issued copy lands before the CTA ends
@@ -720,7 +746,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       }
     }
     if (!ok) {
-      if (issuer) atomicOr(p.err, 2u);
+      if (issuer) atomicOr(err, 2u);
       *abort_flag = 1;
     }
     if (issuer) mma_commit(drain);   // no product still writes TMEM when it is freed
@@ -749,7 +775,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       for (int it = 0; it < iters; it += p.chunk) {
         const bool got = mbar_wait(&tfull[buf], acc_phase, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
-          if (lane == 0) atomicOr(p.err, 4u);
+          if (lane == 0) atomicOr(err, 4u);
           *abort_flag = 1;
           ok = false;
           break;
@@ -788,7 +814,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
           if (g == 0.f) x = 0.f;
           if (in && i < p.n_rows) {
             bf16* dst = p.p_out + (long long)i * p.p_pitch + v;
-            for (int q = 0; q < p.planes; ++q) {
+            for (int q = 0; q < p.p_planes; ++q) {
               const bf16 y = __float2bfloat16_rn(x);
               dst[q * p.p_plane] = y;
               x -= __bfloat162float(y);
@@ -817,9 +843,121 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (own_order && threadIdx.x == 0) p.block_err[blockIdx.x] = s_err;
   if (warp == 1) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(SM::COLS) : "memory");
   }
+}
+
+// ---------------------------------------------------------------------------
+// The loss of up to 16 fp32 rows: bound by reading the fp32 head once, which
+// splitting it into bf16 terms would not allow (13 rows, 43440 x 1704: 292 us
+// that way).  Plain fp32 multiply-adds: the hidden rows in shared memory, a
+// warp four vocabulary entries at a time so that every value read from there
+// meets four head values; the 4 x NT sums are spread over the lanes while they
+// are added up across the warp, and each lane keeps (max, sum) of one row.
+constexpr int F32_FEW_ROWS = 16;
+constexpr int F32_FEW_THREADS = 384;   // 168 registers: the sums stay in them
+
+// Sum over the lanes of N values each; lane l ends with values l, l + 32, ...
+// (N a multiple of 32) in v[0 .. N/32-1].
+template <int N>
+__device__ __forceinline__ void spread_sum(float* v, int lane) {
+#pragma unroll
+  for (int o = 16, n = N; o; o >>= 1, n >>= 1) {
+    // keep the half of the values whose index has the lane's bit o
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      if (i < n / 2) {
+        // indices are blocks of 32: bit o of the index <-> bit o of the lane
+        const int blk = i / o, in = i % o;
+        const float a = v[blk * 2 * o + in], b = v[blk * 2 * o + in + o];
+        const bool up = lane & o;
+        const float mine = up ? b : a, other = up ? a : b;
+        v[i] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+      }
+    }
+  }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(F32_FEW_THREADS, 1) token_loss_f32_few_kernel(const LossParams p, const float* hidden,
+                                                                               const float* head) {
+  extern __shared__ __align__(16) float s_h[];   // [NT][d]
+  constexpr int N = 4 * NT;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int d = p.d;
+  for (int k = threadIdx.x * 4; k < NT * d; k += F32_FEW_THREADS * 4) {
+    const int r = k / d;
+    // a row without a target counts for nothing, whatever it holds
+    const bool ok = r < p.n_rows && target_of(p.ids, p.id_bytes, r, p.vocab) >= 0;
+    *reinterpret_cast<float4*>(s_h + k) =
+        ok ? *reinterpret_cast<const float4*>(hidden + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __syncthreads();
+  // value i = 32 u + lane of the sums: entry i / NT, row i % NT
+  constexpr int U = N / 32 > 0 ? N / 32 : 1;
+  const int row = lane % NT;
+  const int target = row < p.n_rows ? target_of(p.ids, p.id_bytes, row, p.vocab) : -1;
+  float m = -INFINITY, sum = 0.f;
+  const int groups = (p.vocab + 3) / 4;
+  for (int g = blockIdx.x * (F32_FEW_THREADS / 32) + warp; g < groups; g += gridDim.x * (F32_FEW_THREADS / 32)) {
+    const float* w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = head + (long long)min(4 * g + e, p.vocab - 1) * d;
+    float2 acc[4][NT];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[e][n] = make_float2(0.f, 0.f);
+    float4 next[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      next[e] = lane * 4 < d ? __ldg(reinterpret_cast<const float4*>(w[e] + lane * 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = lane * 4; c < d; c += 128) {
+      float4 x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = next[e];
+        if (c + 128 < d) next[e] = __ldg(reinterpret_cast<const float4*>(w[e] + c + 128));
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float4 h = *reinterpret_cast<const float4*>(s_h + n * d + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[e][n] = __ffma2_rn(make_float2(x[e].x, x[e].y), make_float2(h.x, h.y), acc[e][n]);
+          acc[e][n] = __ffma2_rn(make_float2(x[e].z, x[e].w), make_float2(h.z, h.w), acc[e][n]);
+        }
+      }
+    }
+    float v[N < 32 ? 32 : N];
+#pragma unroll
+    for (int i = 0; i < (N < 32 ? 32 : N); ++i) v[i] = i < N ? acc[i / NT % 4][i % NT].x + acc[i / NT % 4][i % NT].y : 0.f;
+    spread_sum<(N < 32 ? 32 : N)>(v, lane);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = 32 * u + lane, entry = 4 * g + i / NT;
+      if (i < N && entry < p.vocab) {
+        const float l = v[u] * p.scale;
+        const float nm = fmaxf(m, l), base = nm == -INFINITY ? 0.f : nm;
+        sum = sum * ex2((m - base) * LOG2E) + ex2((l - base) * LOG2E);
+        m = nm;
+        if (entry == target) p.target_logit[row] = l;
+      }
+    }
+  }
+  // lanes of the same row
+#pragma unroll
+  for (int o = 16; o >= NT; o >>= 1) {
+    const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, sum, o);
+    const float nm = fmaxf(m, om), base = nm == -INFINITY ? 0.f : nm;
+    sum = sum * ex2((m - base) * LOG2E) + os * ex2((om - base) * LOG2E);
+    m = nm;
+  }
+  if (lane < NT && row < p.n_rows)
+    p.part[(long long)(blockIdx.x * (F32_FEW_THREADS / 32) + warp) * p.part_pitch + row] = make_float2(m, sum);
+  if (threadIdx.x == 0) p.block_err[blockIdx.x] = 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -962,16 +1100,32 @@ __global__ void __launch_bounds__(256) split_terms_kernel(const float* x, bf16* 
   }
 }
 
-// Joins the tiles' (max, sum) of each row: rb rows per block, 1024 / rb
-// threads share a row's tiles and meet in shared memory.  The order of the
-// sums is fixed.
-__global__ void __launch_bounds__(1024) join_lse_kernel(const float2* part, int part_pitch, int n_parts,
-                                                        const float* target_logit, const int* n_valid, const int* perm,
-                                                        int rb, float* loss, float* lse, const unsigned* err) {
+// Joins the (max, sum) of each row: rb rows per block, 1024 / rb threads share a
+// row's parts and meet in shared memory.  The order of the sums is fixed.
+// Ordered rows: n_valid of them, their places in perm.  Rows in their own order
+// (ids): those with a target; the blocks' error words become the call's.
+struct JoinParams {
+  const float2* part; int part_pitch; int n_parts;
+  const float* target_logit; const int* n_valid; const int* perm;
+  int rb;
+  float* loss; float* lse;
+  unsigned* err;
+  const void* ids; int id_bytes; int n, vocab; const unsigned* block_err; int blocks;
+};
+
+__global__ void __launch_bounds__(1024) join_lse_kernel(const JoinParams p) {
   __shared__ float2 s[1024];
-  const int x = threadIdx.x % rb, y = threadIdx.x / rb, ny = 1024 / rb;
-  const int row = blockIdx.x * rb + x;
-  const bool in = row < *n_valid;
+  const int x = threadIdx.x % p.rb, y = threadIdx.x / p.rb, ny = 1024 / p.rb;
+  const int row = blockIdx.x * p.rb + x;
+  const bool in = p.ids ? row < p.n && target_of(p.ids, p.id_bytes, row, p.vocab) >= 0 : row < *p.n_valid;
+  bool bad;
+  if (p.ids) {
+    const unsigned e = (int)threadIdx.x < p.blocks ? p.block_err[threadIdx.x] : 0;
+    bad = __syncthreads_or(e != 0) != 0;
+    if (threadIdx.x == 0 && blockIdx.x == 0) *p.err = bad;
+  } else {
+    bad = *p.err != 0;
+  }
   float m = -INFINITY, sum = 0.f;
   auto add = [&](float2 o) {
     const float nm = fmaxf(m, o.x);
@@ -980,13 +1134,13 @@ __global__ void __launch_bounds__(1024) join_lse_kernel(const float2* part, int 
     m = nm;
   };
   if (in) {
-    for (int i0 = y; i0 < n_parts; i0 += 8 * ny) {   // eight at a time: one running maximum for all
+    for (int i0 = y; i0 < p.n_parts; i0 += 8 * ny) {   // eight at a time: one running maximum for all
       float2 o[8];
       float nm = m;
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int i = i0 + u * ny;
-        o[u] = i < n_parts ? part[(long long)i * part_pitch + row] : make_float2(-INFINITY, 0.f);
+        o[u] = i < p.n_parts ? p.part[(long long)i * p.part_pitch + row] : make_float2(-INFINITY, 0.f);
         nm = fmaxf(nm, o[u].x);
       }
       const float base = nm == -INFINITY ? 0.f : nm;
@@ -1000,27 +1154,37 @@ __global__ void __launch_bounds__(1024) join_lse_kernel(const float2* part, int 
   __syncthreads();
   for (int h = ny / 2; h; h >>= 1) {
     if (y < h) {
-      add(s[threadIdx.x + h * rb]);
+      add(s[threadIdx.x + h * p.rb]);
       s[threadIdx.x] = make_float2(m, sum);
     }
     __syncthreads();
   }
-  if (y == 0 && in) {
+  if (y != 0) return;
+  if (in) {
     const float ls = logf(sum);
-    const bool bad = *err != 0;
-    loss[perm[row]] = bad ? NAN : (m - target_logit[row]) + ls;
-    lse[perm[row]] = bad ? NAN : m + ls;
+    const int at = p.ids ? row : p.perm[row];
+    p.loss[at] = bad ? NAN : (m - p.target_logit[row]) + ls;
+    p.lse[at] = bad ? NAN : m + ls;
+  } else if (p.ids && row < p.n) {
+    p.loss[row] = 0.f;
+    p.lse[row] = 0.f;
   }
 }
 
 // dH rows back in their order: the splits' partial sums added in order, times
-// the weights' common factor.  After a wait that ran out, NaN.
+// the weights' common factor.  After a wait that ran out, NaN there and in the
+// head's gradient.  Either may be null.
 template <typename T>
 __global__ void __launch_bounds__(256) join_rows_kernel(const float* part, int splits, int n, int d, const int* perm,
                                                         const int* n_valid, const float* g_max, float scale,
-                                                        const unsigned* err, T* out) {
+                                                        const unsigned* err, T* out, T* head, long long head_n) {
   const int nv = *n_valid;
   const bool bad = *err != 0;
+  if (bad && head) {
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < head_n; i += (long long)gridDim.x * 256)
+      head[i] = (T)NAN;
+  }
+  if (!out) return;
   const float f = *g_max * scale;
   const int vecs = d / 8;
   const long long total = (long long)n * vecs, plane = (long long)n * d;
@@ -1052,14 +1216,6 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const float* part, int s
   }
 }
 
-// After a wait that ran out: NaN in the head's gradient too.
-template <typename T>
-__global__ void __launch_bounds__(256) fail_head_kernel(const unsigned* err, T* out, long long n) {
-  if (*err == 0) return;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256)
-    out[i] = (T)NAN;
-}
-
 // ---------------------------------------------------------------------------
 // Host side.
 
@@ -1073,17 +1229,28 @@ int div_up(int a, int b) { return (a + b - 1) / b; }
 // Blocks of the few-rows kernel: one per SM of the B200, a vocabulary tile of 128 each at least.
 int few_blocks(int v) { return div_up(v, 128) < 148 ? div_up(v, 128) : 148; }
 
+// Whether the loss of fp32 rows runs on plain multiply-adds (the rows have to
+// fit the shared memory, up to 3200 columns for 16 of them).
+int f32_few_rows(int n) { return n <= 4 ? 4 : F32_FEW_ROWS; }
+bool f32_few(bool f32, int n, int d, bool grad) {
+  return f32 && !grad && n <= F32_FEW_ROWS && (size_t)f32_few_rows(n) * d * 4 <= 200 * 1024;
+}
+
 // Workspace of one call, laid out in order.
 struct Layout {
-  int planes, rows, pieces, vc, splits, k_split, n_parts;
-  size_t n_valid, g_max, rows_b, perm, target, g, lse, tlogit, part, head, p, dh, total;
+  int planes, p_planes, rows, pieces, vc, splits, k_split, n_parts;
+  size_t block_err, n_valid, g_max, rows_b, perm, target, g, lse, tlogit, part, head, p, dh, total;
   Layout(int n, int v, int d, bool f32, bool grad) {
     planes = f32 ? 3 : 1;
+    // P beside bf16 operands: one bf16 term; two for few rows, where the products
+    // are not what bounds the gradient and few roundings average out
+    p_planes = f32 ? 3 : (n <= 128 ? 2 : 1);
+    const bool simt = f32_few(f32, n, d, grad);
     rows = grad ? n : (n < LOSS_ROWS ? n : LOSS_ROWS);
-    n_parts = n <= FEW_ROWS ? 4 * few_blocks(v) : 2 * div_up(v, TILE);
+    n_parts = simt ? 148 * (F32_FEW_THREADS / 32) : (n <= FEW_ROWS ? 4 * few_blocks(v) : 2 * div_up(v, TILE));
     vc = v; pieces = 1; splits = k_split = 0;
     if (grad) {
-      long long w = P_BYTES / ((long long)n * 2 * planes) / TILE * TILE;
+      long long w = P_BYTES / ((long long)n * 2 * p_planes) / TILE * TILE;
       if (w < TILE) w = TILE;
       if (w < v) {
         pieces = div_up(v, (int)w);
@@ -1102,6 +1269,7 @@ struct Layout {
     }
     size_t o = 256;   // the error word
     auto take = [&](size_t bytes) { const size_t at = o; o += up256(bytes); return at; };
+    block_err = take(148 * 4);
     n_valid = take(4);
     g_max = take(4);
     rows_b = take((size_t)planes * rows * d * 2);
@@ -1111,8 +1279,8 @@ struct Layout {
     lse = take(grad ? (size_t)rows * 4 : 0);
     tlogit = take(grad ? 0 : (size_t)rows * 4);
     part = take(grad ? 0 : (size_t)n_parts * rows * 8);
-    head = take(f32 ? (size_t)3 * v * d * 2 : 0);
-    p = take(grad ? (size_t)planes * n * round_up(vc, 64) * 2 : 0);
+    head = take(f32 && !simt ? (size_t)3 * v * d * 2 : 0);
+    p = take(grad ? (size_t)p_planes * n * round_up(vc, 64) * 2 : 0);
     dh = take(grad ? (size_t)splits * n * d * 4 : 0);
     total = o;
   }
@@ -1182,6 +1350,15 @@ cudaError_t launch_few(const LossMaps& maps, const LossParams& p, cudaStream_t s
   return cudaGetLastError();
 }
 
+template <int NT>
+cudaError_t launch_f32_few(const LossParams& p, const void* hidden, const void* head, cudaStream_t st) {
+  const int smem = NT * p.d * 4;
+  cudaError_t e = cudaFuncSetAttribute(token_loss_f32_few_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  token_loss_f32_few_kernel<NT><<<148, F32_FEW_THREADS, smem, st>>>(p, (const float*)hidden, (const float*)head);
+  return cudaGetLastError();
+}
+
 // Hidden rows as the few-rows kernel reads them: boxes of NT rows.
 cudaError_t few_map(CUtensorMap* map, const void* rows, int n, int d, int planes) {
   return make_map(map, rows, false, d, d, n, planes, BK, n <= 16 ? 16 : FEW_ROWS);
@@ -1248,10 +1425,48 @@ extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d
   if (workspace_bytes < L.total) return ARMT_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   char* ws = (char*)workspace;
+  JoinParams jp{};
+  jp.part = (const float2*)(ws + L.part); jp.n_parts = L.n_parts; jp.target_logit = (const float*)(ws + L.tlogit);
+  jp.err = (unsigned*)ws; jp.vocab = vocab;
+  LossParams p{};
+  p.d = d; p.vocab = vocab; p.planes = L.planes; p.v0 = 0; p.vc = vocab; p.scale = scale;
+  p.part = (float2*)(ws + L.part); p.target_logit = (float*)(ws + L.tlogit); p.err = (unsigned*)ws;
+  auto join = [&](int rows, int r0) {
+    jp.rb = 32;
+    while (jp.rb > 1 && jp.rb / 2 >= rows) jp.rb /= 2;
+    jp.part_pitch = rows;
+    jp.n = rows;
+    jp.loss = loss + r0;
+    jp.lse = lse + r0;
+    join_lse_kernel<<<div_up(rows, jp.rb), 1024, 0, st>>>(jp);
+    return cudaGetLastError();
+  };
+  LossMaps maps{};
+  const bool simt = f32_few(f32, n, d, false);
+  if (simt || (!f32 && n <= FEW_ROWS)) {   // few rows, in their own order: two launches
+    p.n_rows = p.part_pitch = n;
+    p.ids = jp.ids = targets;
+    p.id_bytes = jp.id_bytes = target_bytes;
+    p.block_err = (unsigned*)(ws + L.block_err);
+    jp.block_err = p.block_err;
+    p.chunk = FEW_CHUNK;
+    cudaError_t e;
+    if (simt) {
+      jp.blocks = 148;
+      e = n <= 4 ? launch_f32_few<4>(p, hidden, head, st) : launch_f32_few<F32_FEW_ROWS>(p, hidden, head, st);
+    } else {
+      jp.blocks = few_blocks(vocab);
+      e = few_map(&maps.a, hidden, n, d, 1);
+      if (e == cudaSuccess) e = load_map(&maps.b, head, d, d, vocab, 1);
+      if (e == cudaSuccess) e = n <= 16 ? launch_few<LSE, 16>(maps, p, st) : launch_few<LSE, 64>(maps, p, st);
+    }
+    if (e == cudaSuccess) e = join(n, 0);
+    return cuda_status(e);
+  }
   const void* w = nullptr;
   cudaError_t e = head_operand(L, ws, head, vocab, d, f32, &w, st);
-  LossMaps maps{};
   if (e == cudaSuccess) e = load_map(&maps.b, w, d, d, vocab, L.planes);
+  const bool few = n <= FEW_ROWS;   // up to 64 rows: bound by reading the head
   for (int r0 = 0; r0 < n && e == cudaSuccess; r0 += L.rows) {
     const int nr = n - r0 < L.rows ? n - r0 : L.rows;
     RowParams rp{};
@@ -1262,23 +1477,17 @@ extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d
     rp.n_valid = (int*)(ws + L.n_valid); rp.err = (unsigned*)ws;
     rp.loss_out = loss + r0; rp.lse_out = lse + r0;
     e = launch_order_rows(rp, f32, st);
-    // up to 64 rows: bound by reading the head (loss_one: 125 us in pairs)
-    const bool few = n <= FEW_ROWS;
     if (e == cudaSuccess)
       e = few ? few_map(&maps.a, ws + L.rows_b, nr, d, L.planes) : load_map(&maps.a, ws + L.rows_b, d, d, nr, L.planes);
     if (e != cudaSuccess) break;
-    LossParams p{};
-    p.n_rows = nr; p.d = d; p.vocab = vocab; p.planes = L.planes; p.v0 = 0; p.vc = vocab;
-    p.chunk = f32 ? F32_CHUNK : LSE_CHUNK; p.scale = scale; p.n_valid = rp.n_valid; p.target = rp.target;
-    p.part = (float2*)(ws + L.part); p.part_pitch = nr; p.target_logit = (float*)(ws + L.tlogit); p.err = rp.err;
+    p.n_rows = p.part_pitch = nr;
+    p.n_valid = jp.n_valid = rp.n_valid;
+    p.target = rp.target;
+    jp.perm = rp.perm;
+    p.chunk = few ? FEW_CHUNK : (f32 ? F32_CHUNK : LSE_CHUNK);
     if (few) e = nr <= 16 ? launch_few<LSE, 16>(maps, p, st) : launch_few<LSE, 64>(maps, p, st);
     else e = launch_products<LSE>(maps, p, (long long)div_up(nr, TILE) * div_up(vocab, TILE), st);
-    if (e != cudaSuccess) break;
-    int rb = 32;
-    while (rb > 1 && rb / 2 >= nr) rb /= 2;
-    join_lse_kernel<<<div_up(nr, rb), 1024, 0, st>>>(p.part, nr, L.n_parts, p.target_logit, rp.n_valid, rp.perm, rb,
-                                                     loss + r0, lse + r0, rp.err);
-    e = cudaGetLastError();
+    if (e == cudaSuccess) e = join(nr, r0);
   }
   return cuda_status(e);
 }
@@ -1316,7 +1525,7 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
   if (e == cudaSuccess && d_head) e = make_map(&mg.out0, d_head, f32, d, d, vocab, 1, f32 ? 32 : 64, 32);
   if (e == cudaSuccess && d_hidden) e = make_map(&mg.out1, ws + L.dh, true, d, d, n, L.splits, 32, 32);
   LossParams p{};
-  p.n_rows = n; p.d = d; p.vocab = vocab; p.planes = L.planes; p.scale = scale;
+  p.n_rows = n; p.d = d; p.vocab = vocab; p.planes = L.planes; p.p_planes = L.p_planes; p.scale = scale;
   p.n_valid = rp.n_valid; p.target = rp.target; p.lse = rp.lse; p.g = rp.g; p.g_max = rp.g_max; p.err = rp.err;
   p.want_dw = d_head != nullptr; p.want_dh = d_hidden != nullptr; p.dw_bf16 = !f32; p.k_split = L.k_split;
   const bool few = n <= FEW_ROWS;
@@ -1327,8 +1536,8 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     p.vc = vocab - v0 < L.vc ? vocab - v0 : L.vc;
     p.splits = div_up(p.vc, L.k_split);
     p.dh_add = v0 > 0;
-    e = load_map(&mg.a, ws + L.p, p.vc, pitch, n, L.planes);
-    if (e == cudaSuccess) e = make_map(&mp.out0, ws + L.p, false, p.vc, pitch, n, L.planes, 64, 32);
+    e = load_map(&mg.a, ws + L.p, p.vc, pitch, n, L.p_planes);
+    if (e == cudaSuccess) e = make_map(&mp.out0, ws + L.p, false, p.vc, pitch, n, L.p_planes, 64, 32);
     p.chunk = f32 ? F32_CHUNK : 1 << 30;
     const int nt = div_up(p.vc, TILE);
     p.p_out = (bf16*)(ws + L.p);
@@ -1340,22 +1549,17 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     const long long jobs = (p.want_dw ? (long long)nt * dt : 0) + (p.want_dh ? (long long)mt * dt * p.splits : 0);
     if (e == cudaSuccess) e = launch_products<GRAD>(mg, p, jobs, st);
   }
-  if (e == cudaSuccess && d_hidden) {
+  if (e == cudaSuccess) {
     const long long blocks = ((long long)n * (d / 8) + 255) / 256;
-    const int grid = (int)(blocks < 148 * 16 ? blocks : 148 * 16);
+    const int grid = d_hidden ? (int)(blocks < 148 * 16 ? blocks : 148 * 16) : 148;
     const float* part = (const float*)(ws + L.dh);
+    const long long head_n = (long long)vocab * d;
     if (f32)
       join_rows_kernel<float><<<grid, 256, 0, st>>>(part, L.splits, n, d, rp.perm, rp.n_valid, rp.g_max, scale, rp.err,
-                                                    (float*)d_hidden);
+                                                    (float*)d_hidden, (float*)d_head, head_n);
     else
       join_rows_kernel<bf16><<<grid, 256, 0, st>>>(part, L.splits, n, d, rp.perm, rp.n_valid, rp.g_max, scale, rp.err,
-                                                   (bf16*)d_hidden);
-    e = cudaGetLastError();
-  }
-  if (e == cudaSuccess && d_head) {
-    const long long total = (long long)vocab * d;
-    if (f32) fail_head_kernel<float><<<148, 256, 0, st>>>(rp.err, (float*)d_head, total);
-    else fail_head_kernel<bf16><<<148, 256, 0, st>>>(rp.err, (bf16*)d_head, total);
+                                                   (bf16*)d_hidden, (bf16*)d_head, head_n);
     e = cudaGetLastError();
   }
   return cuda_status(e);

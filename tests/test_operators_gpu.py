@@ -68,9 +68,10 @@ def grad_reference(ids, d_out, v, scale, base):
 EMBED_GRAD = [
     # n, v, d, how the ids fall
     (1, 1, 8, "uniform"), (1, 300, 64, "uniform"), (67, 515, 64, "uniform"),
-    (2048, 1000, 72, "skewed"),            # most tokens of the one-launch form
-    (2048, 40, 64, "one"),
-    (2049, 1000, 72, "skewed"),            # fewest of the sorted one
+    (128, 100, 72, "skewed"),              # most tokens of the one-launch form
+    (128, 40, 64, "one"),
+    (129, 100, 72, "skewed"),              # fewest of the sorted one
+    (2048, 1000, 72, "skewed"), (2048, 40, 64, "one"), (2049, 1000, 72, "skewed"),
     (2049, 1, 8, "uniform"),               # one row takes everything
     (5000, 511, 64, "uniform"), (5000, 512, 64, "uniform"), (5000, 262145, 8, "uniform"),   # 1, 2, 3 passes
     (20011, 3001, 256, "skewed"), (9000, 100, 2048, "one"), (6400, 100, 64, "blocks"),
@@ -219,12 +220,13 @@ def loss_reference(hidden, head, targets, scale):
 
 
 def logit_error(A, d, planes):
-    """A logit's error: a chunk of at most 16 instructions, each truncated (2 u) once in the
-    instruction's own sum and once in the accumulator, chunks added to nearest; fp32 operands:
-    six products, and three terms of 24 bits less what the dropped products hold."""
+    """A logit's error: a chunk of at most 32 instructions (K = 512), each truncated (2 u) once
+    in the instruction's own sum and once in the accumulator, chunks (of 128 at least) added
+    to nearest; fp32 operands: six products, and three terms of 24 bits less what the dropped
+    products hold.  Plain multiply-adds (d / 128 a lane, 5 sums) stay below that."""
     terms = 6 if planes == 3 else 1
-    chunks = math.ceil(terms * math.ceil(d / 64) / 4)
-    return A * ((32 * 2 + chunks) * U + (8 * U if planes == 3 else 0))
+    chunks = math.ceil(terms * math.ceil(d / 64) / 2)
+    return A * ((64 * 2 + chunks) * U + (8 * U if planes == 3 else 0))
 
 
 def loss_inputs(seed, n, v, d, dtype, idt=torch.int64, ignored=0.2):
@@ -292,6 +294,7 @@ LOSS = [
     # n, v, d
     (1, 1, 8), (1, 300, 64), (2, 255, 72), (3, 256, 64), (5, 257, 136), (127, 512, 256), (128, 1000, 64),
     (129, 1023, 328), (255, 1025, 64), (257, 777, 512), (300, 5003, 128), (64, 33000, 64), (1030, 259, 2048),
+    (4, 20000, 72), (16, 700, 200), (17, 515, 64), (65, 300, 64), (16, 300, 3208), (130, 2500, 136), (128, 700, 384),
 ]
 
 
