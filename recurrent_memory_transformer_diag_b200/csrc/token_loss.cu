@@ -48,7 +48,6 @@ using namespace tc;
 
 constexpr int TILE = 256;              // rows and columns of a CTA pair's tile (each CTA: 128 rows)
 constexpr int BK = 64;                 // 64 bf16 = 128 bytes = one swizzle row
-constexpr int STAGES = 6;
 constexpr int BOX_BYTES = 64 * BK * 2; // one copied box: 64 x 64 bf16
 constexpr int STAGE_BYTES = 4 * BOX_BYTES;   // two boxes of A, two of B
 constexpr int EPI_WARPS = 8;
@@ -57,19 +56,25 @@ constexpr int NUM_THREADS = 128 + 32 * EPI_WARPS;   // a control warpgroup and t
 // warpgroup gives its to the epilogue, which holds 128 sums a thread
 constexpr int CTRL_REGS = 40, EPI_REGS = 232;
 static_assert(128 * CTRL_REGS + 32 * EPI_WARPS * EPI_REGS <= 168 * NUM_THREADS, "register split");
-constexpr int SLOT_BYTES = 4096;       // per epilogue warp: 32 rows x 128 bytes of output
-constexpr int SLOT_OFFSET = STAGES * STAGE_BYTES;
-constexpr int BAR_OFFSET = SLOT_OFFSET + EPI_WARPS * SLOT_BYTES;
-constexpr int SMEM_TOTAL = BAR_OFFSET + 256 + 1024;   // + alignment slack
-static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory per CTA");
+constexpr int SLOT_BYTES = 4096;       // 32 rows x 128 bytes of output; two per epilogue warp
+
+enum Role { LSE = 0, PROB = 1, GRAD = 2 };
+
+// Shared memory: LSE writes no tile and has all of it for stages in flight.
+template <int ROLE>
+struct Smem {
+  static constexpr int STAGES = ROLE == LSE ? 7 : 5;
+  static constexpr int SLOTS = STAGES * STAGE_BYTES;
+  static constexpr int BARS = SLOTS + (ROLE == LSE ? 0 : 2 * EPI_WARPS * SLOT_BYTES);
+  static constexpr int TOTAL = BARS + 256 + 1024;   // + alignment slack
+  static_assert(TOTAL <= 227 * 1024, "shared memory per CTA");
+};
 
 constexpr int ROW_GROUP = 32;          // row tiles that share a vocabulary tile before the next one
 constexpr int LSE_CHUNK = 8;           // k-blocks per accumulator of the loss's logits (K = 512)
 constexpr int FEW_CHUNK = 2;           // ... of few rows' logits, where it costs nothing (K = 128)
 constexpr int F32_CHUNK = 4;           // ... of everything that fp32 operands give (K = 256)
 constexpr float LOG2E = 1.4426950408889634f;
-
-enum Role { LSE = 0, PROB = 1, GRAD = 2 };
 
 struct LossParams {
   int n_rows, d, vocab;
@@ -84,7 +89,7 @@ struct LossParams {
   float2* part; int part_pitch; float* target_logit;
   // PROB
   const float* lse; const float* g;
-  bf16* p_out; int p_pitch; long long p_plane;   // few rows: P is written without a tensor map
+  bf16* p_out; int p_trans;   // few rows: P is kept transposed, [term][entry][NT], each thread writing its entry
   // few rows, LSE: rows in their own order, targets as the caller gave them
   const void* ids; int id_bytes; unsigned* block_err;
   // GRAD
@@ -203,9 +208,9 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* s
                : "memory");
 }
 
-// The slot of this warp may be written again (its last store has been read).
+// The warp's other slot may be written (all but the last store have been read).
 __device__ __forceinline__ void slot_free(int lane) {
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
   __syncwarp();
 }
 
@@ -225,7 +230,7 @@ __device__ __forceinline__ void slot_store(const CUtensorMap* map, uint8_t* slot
   }
 }
 
-// 64 values per lane (a row each) as bf16: columns c0 .. c0+63 of rows c1 .. c1+31.
+// 64 values per lane (a row each) as bf16, through one of the warp's two slots: columns c0 .. c0+63 of rows c1 .. c1+31.
 __device__ __forceinline__ void emit_bf16x64(const CUtensorMap* map, uint8_t* slot, int lane, const float2* v, int c0,
                                              int c1, int c2) {
   slot_free(lane);
@@ -264,7 +269,8 @@ __device__ __forceinline__ float ex2(float x) {
 template <int ROLE>
 __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps& maps, const Job& j, int nv,
                                             float2 (&sums)[64], int row_in_tile, int half, int lane,
-                                            uint8_t* slot) {
+                                            uint8_t* slots, int& turn) {
+  auto slot = [&] { return slots + (turn ^= 1) * SLOT_BYTES; };
   const int row = j.m0 + row_in_tile;
   const int wrow0 = row - lane;
   const int col0 = j.n0 + half * 128;
@@ -338,7 +344,7 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
     for (int h = 0; h < 2; ++h) {
       if (wrow0 >= p.n_rows || pc + 64 * h >= p.vc) continue;   // nothing of this box is in P
       for (int t = 0; t < p.p_planes; ++t) {
-        emit_bf16x64(&maps.out0, slot, lane, sums + 32 * h, pc + 64 * h, wrow0, t);
+        emit_bf16x64(&maps.out0, slot(), lane, sums + 32 * h, pc + 64 * h, wrow0, t);
         if (t + 1 < p.p_planes) {   // what the term just written leaves of the value
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -358,19 +364,19 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
       if (p.dw_bf16) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          if (col0 + 64 * h < p.d) emit_bf16x64(&maps.out0, slot, lane, sums + 32 * h, col0 + 64 * h, p.v0 + wrow0, 0);
+          if (col0 + 64 * h < p.d) emit_bf16x64(&maps.out0, slot(), lane, sums + 32 * h, col0 + 64 * h, p.v0 + wrow0, 0);
       } else {
 #pragma unroll
         for (int h = 0; h < 4; ++h)
           if (col0 + 32 * h < p.d)
-            emit_f32x32(&maps.out0, slot, lane, sums + 16 * h, col0 + 32 * h, p.v0 + wrow0, 0, false);
+            emit_f32x32(&maps.out0, slot(), lane, sums + 16 * h, col0 + 32 * h, p.v0 + wrow0, 0, false);
       }
     } else {
       if (wrow0 >= p.n_rows) return;
 #pragma unroll
       for (int h = 0; h < 4; ++h)
         if (col0 + 32 * h < p.d)
-          emit_f32x32(&maps.out1, slot, lane, sums + 16 * h, col0 + 32 * h, wrow0, j.split, p.dh_add != 0);
+          emit_f32x32(&maps.out1, slot(), lane, sums + 16 * h, col0 + 32 * h, wrow0, j.split, p.dh_add != 0);
     }
   }
 }
@@ -391,9 +397,11 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
 template <int ROLE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     token_loss_kernel(const __grid_constant__ LossMaps maps, const LossParams p) {
+  using SM = Smem<ROLE>;
+  constexpr int STAGES = SM::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + BAR_OFFSET);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::BARS);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
@@ -451,32 +459,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
     for (int t = cid; t < jobs.total && ok; t += ncl) {
       const Job j = jobs.get(p, nv, t);
-      const bool a_mn = ROLE == GRAD && j.dw, b_mn = ROLE == GRAD;
+      const bool a_mn = ROLE == GRAD && j.dw != (p.p_trans != 0), b_mn = ROLE == GRAD;
       const CUtensorMap* ma = &maps.a;
       const CUtensorMap* mb = ROLE == GRAD && j.dw ? &maps.c : &maps.b;
       const int am = j.m0 + (int)rank * 128, bn = j.n0 + (int)rank * (j.n / 2);
-      for (int q = 0; q < products && ok; ++q) {
-        const int ta = term_a(q, products), tb = term_b(q, products);
-        for (int kb = 0; kb < j.kblocks; ++kb) {
-          if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
-          armed &= ~(1u << stage);
-          uint8_t* sa = smem + stage * STAGE_BYTES;
-          if (issuer) {
-            // both CTAs' copies
-            if (leader) mbar_expect_tx(&full[stage], 2 * (2 * BOX_BYTES + j.n / 128 * BOX_BYTES));
-            const uint32_t fb = full0 + (uint32_t)(stage * sizeof(uint64_t));
-            const int ka = j.ka + kb * BK, kbb = j.kb + kb * BK;
+      // the products of a k-block one after another: its tiles come from L2 again
+      for (int kb = 0, q = 0; kb < j.kblocks;) {
+        if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+        armed &= ~(1u << stage);
+        uint8_t* sa = smem + stage * STAGE_BYTES;
+        if (issuer) {
+          const int ta = term_a(q, products), tb = term_b(q, products);
+          // both CTAs' copies
+          if (leader) mbar_expect_tx(&full[stage], 2 * (2 * BOX_BYTES + j.n / 128 * BOX_BYTES));
+          const uint32_t fb = full0 + (uint32_t)(stage * sizeof(uint64_t));
+          const int ka = j.ka + kb * BK, kbb = j.kb + kb * BK;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              tma_load_3d_pair(ma, fb, sa + h * BOX_BYTES, a_mn ? am + 64 * h : ka, a_mn ? ka : am + 64 * h, ta);
-              if (128 * h < j.n)
-                tma_load_3d_pair(mb, fb, sa + (2 + h) * BOX_BYTES, b_mn ? bn + 64 * h : kbb, b_mn ? kbb : bn + 64 * h,
-                                 tb);
-            }
+          for (int h = 0; h < 2; ++h) {
+            tma_load_3d_pair(ma, fb, sa + h * BOX_BYTES, a_mn ? am + 64 * h : ka, a_mn ? ka : am + 64 * h, ta);
+            if (128 * h < j.n)
+              tma_load_3d_pair(mb, fb, sa + (2 + h) * BOX_BYTES, b_mn ? bn + 64 * h : kbb, b_mn ? kbb : bn + 64 * h,
+                               tb);
           }
-          armed |= 1u << stage;
-          if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
+        armed |= 1u << stage;
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        if (++q == products) { q = 0; ++kb; }
       }
     }
     if (!ok) {
@@ -501,7 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       bool ok = true;
       for (int t = cid; t < jobs.total && ok; t += ncl) {
         const Job j = jobs.get(p, nv, t);
-        const bool a_mn = ROLE == GRAD && j.dw, b_mn = ROLE == GRAD;
+        const bool a_mn = ROLE == GRAD && j.dw != (p.p_trans != 0), b_mn = ROLE == GRAD;
         const uint32_t idesc = idesc_f16(j.n, 1, TILE) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
         const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
         const int iters = products * j.kblocks;
@@ -546,8 +554,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     const int half = (warp - 4) >> 2;
     const int row_in_tile = (int)rank * 128 + quarter * 32 + lane;
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
-    uint8_t* slot = smem + SLOT_OFFSET + (warp - 4) * SLOT_BYTES;
-    int buf = 0;
+    uint8_t* slots = smem + SM::SLOTS + (warp - 4) * 2 * SLOT_BYTES;
+    int buf = 0, turn = 0;
     uint32_t acc_phase = 0;
     bool ok = !skip;
     for (int t = cid; t < jobs.total && ok; t += ncl) {
@@ -578,7 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
         if (++buf == 2) { buf = 0; acc_phase ^= 1; }
       }
-      if (ok) finish_tile<ROLE>(p, maps, j, nv, acc, row_in_tile, half, lane, slot);
+      if (ok) finish_tile<ROLE>(p, maps, j, nv, acc, row_in_tile, half, lane, slots, turn);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
@@ -686,21 +694,20 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     bool ok = true;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const int v = p.v0 + t * 128;
-      for (int q = 0; q < products && ok; ++q) {
-        const int ta = term_a(q, products), tb = term_b(q, products);
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
-          armed &= ~(1u << stage);
-          uint8_t* sa = smem + stage * SM::STAGE;
-          if (issuer) {
-            mbar_expect_tx(&full[stage], SM::STAGE);
-            tma_load_3d(&maps.b, &full[stage], sa, kb * BK, v, tb);
-            tma_load_3d(&maps.b, &full[stage], sa + BOX_BYTES, kb * BK, v + 64, tb);
-            tma_load_3d(&maps.a, &full[stage], sa + 2 * BOX_BYTES, kb * BK, 0, ta);
-          }
-          armed |= 1u << stage;
-          if (++stage == SM::N_STAGES) { stage = 0; phase ^= 1; }
+      for (int kb = 0, q = 0; kb < kblocks;) {
+        if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+        armed &= ~(1u << stage);
+        uint8_t* sa = smem + stage * SM::STAGE;
+        if (issuer) {
+          const int ta = term_a(q, products), tb = term_b(q, products);
+          mbar_expect_tx(&full[stage], SM::STAGE);
+          tma_load_3d(&maps.b, &full[stage], sa, kb * BK, v, tb);
+          tma_load_3d(&maps.b, &full[stage], sa + BOX_BYTES, kb * BK, v + 64, tb);
+          tma_load_3d(&maps.a, &full[stage], sa + 2 * BOX_BYTES, kb * BK, 0, ta);
         }
+        armed |= 1u << stage;
+        if (++stage == SM::N_STAGES) { stage = 0; phase ^= 1; }
+        if (++q == products) { q = 0; ++kb; }
       }
     }
     if (!ok) {
@@ -811,14 +818,21 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
           const float g = s_g[i];
           float x = g * ex2((l - s_lse[i]) * LOG2E);
           if (hit) x -= g;
-          if (g == 0.f) x = 0.f;
-          if (in && i < p.n_rows) {
-            bf16* dst = p.p_out + (long long)i * p.p_pitch + v;
-            for (int q = 0; q < p.p_planes; ++q) {
-              const bf16 y = __float2bfloat16_rn(x);
-              dst[q * p.p_plane] = y;
-              x -= __bfloat162float(y);
-            }
+          acc[i] = g == 0.f ? 0.f : x;
+        }
+      }
+      if constexpr (ROLE == PROB) {
+        for (int q = 0; q < p.p_planes; ++q) {
+          bf16* dst = p.p_out + ((long long)q * p.vc + v) * NT;
+#pragma unroll
+          for (int i = 0; i < NT; i += 8) {
+            Vec8<bf16> y;
+            y.set(acc + i);
+            if (in) y.store(dst + i);
+            float hi[8];
+            y.get(hi);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[i + k] -= hi[k];
           }
         }
       }
@@ -1186,32 +1200,27 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const float* part, int s
   }
   if (!out) return;
   const float f = *g_max * scale;
-  const int vecs = d / 8;
+  const int vecs = d / 4;
   const long long total = (long long)n * vecs, plane = (long long)n * d;
   for (long long k = (long long)blockIdx.x * 256 + threadIdx.x; k < total; k += (long long)gridDim.x * 256) {
-    const int r = (int)(k / vecs), c = (int)(k - (long long)r * vecs) * 8;
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = bad ? NAN : 0.f;
+    const int r = (int)(k / vecs), c = (int)(k - (long long)r * vecs) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (bad) v = make_float4(NAN, NAN, NAN, NAN);
     if (r < nv && !bad) {
+#pragma unroll 8
       for (int s = 0; s < splits; ++s) {
-        const float4* src = reinterpret_cast<const float4*>(part + s * plane + (long long)r * d + c);
-        const float4 a = src[0], b = src[1];
-        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+        const float4 a = *reinterpret_cast<const float4*>(part + s * plane + (long long)r * d + c);
+        v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= f;
+      v.x *= f; v.y *= f; v.z *= f; v.w *= f;
     }
     T* dst = out + (long long)perm[r] * d + c;
     if constexpr (sizeof(T) == 2) {
-      __align__(16) bf16 t[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = __float2bfloat16_rn(v[i]);
-      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<uint4*>(t);
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     } else {
-      reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      *reinterpret_cast<float4*>(dst) = v;
     }
   }
 }
@@ -1280,7 +1289,7 @@ struct Layout {
     tlogit = take(grad ? 0 : (size_t)rows * 4);
     part = take(grad ? 0 : (size_t)n_parts * rows * 8);
     head = take(f32 && !simt ? (size_t)3 * v * d * 2 : 0);
-    p = take(grad ? (size_t)p_planes * n * round_up(vc, 64) * 2 : 0);
+    p = take(grad ? (size_t)p_planes * (n <= 16 ? 16 : (n <= FEW_ROWS ? FEW_ROWS : n)) * round_up(vc, 64) * 2 : 0);
     dh = take(grad ? (size_t)splits * n * d * 4 : 0);
     total = o;
   }
@@ -1319,12 +1328,12 @@ cudaError_t pairs_on_device(int* out) {
   if (dev < 0 || dev >= MAX_DEVICES) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
   if (!known[dev]) {
-    e = cudaFuncSetAttribute(token_loss_kernel<ROLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+    e = cudaFuncSetAttribute(token_loss_kernel<ROLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<ROLE>::TOTAL);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2, 1, 1);
     cfg.blockDim = dim3(NUM_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = SMEM_TOTAL;
+    cfg.dynamicSmemBytes = Smem<ROLE>::TOTAL;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2; attr.val.clusterDim.y = 1; attr.val.clusterDim.z = 1;
@@ -1370,7 +1379,7 @@ cudaError_t launch_products(const LossMaps& maps, const LossParams& p, long long
   cudaError_t e = pairs_on_device<ROLE>(&pairs);
   if (e != cudaSuccess) return e;
   const int grid = (int)(jobs < pairs ? jobs : pairs);
-  token_loss_kernel<ROLE><<<2 * grid, NUM_THREADS, SMEM_TOTAL, st>>>(maps, p);
+  token_loss_kernel<ROLE><<<2 * grid, NUM_THREADS, Smem<ROLE>::TOTAL, st>>>(maps, p);
   return cudaGetLastError();
 }
 
@@ -1536,13 +1545,14 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     p.vc = vocab - v0 < L.vc ? vocab - v0 : L.vc;
     p.splits = div_up(p.vc, L.k_split);
     p.dh_add = v0 > 0;
-    e = load_map(&mg.a, ws + L.p, p.vc, pitch, n, L.p_planes);
-    if (e == cudaSuccess) e = make_map(&mp.out0, ws + L.p, false, p.vc, pitch, n, L.p_planes, 64, 32);
+    const int nt16 = n <= 16 ? 16 : FEW_ROWS;
+    if (few) e = load_map(&mg.a, ws + L.p, n, nt16, p.vc, L.p_planes);
+    else e = load_map(&mg.a, ws + L.p, p.vc, pitch, n, L.p_planes);
+    if (e == cudaSuccess && !few) e = make_map(&mp.out0, ws + L.p, false, p.vc, pitch, n, L.p_planes, 64, 32);
     p.chunk = f32 ? F32_CHUNK : 1 << 30;
     const int nt = div_up(p.vc, TILE);
     p.p_out = (bf16*)(ws + L.p);
-    p.p_pitch = pitch;
-    p.p_plane = (long long)n * pitch;
+    p.p_trans = few;
     if (e == cudaSuccess)
       e = !few ? launch_products<PROB>(mp, p, (long long)mt * nt, st)
                : (n <= 16 ? launch_few<PROB, 16>(mp, p, st) : launch_few<PROB, 64>(mp, p, st));
@@ -1550,7 +1560,7 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     if (e == cudaSuccess) e = launch_products<GRAD>(mg, p, jobs, st);
   }
   if (e == cudaSuccess) {
-    const long long blocks = ((long long)n * (d / 8) + 255) / 256;
+    const long long blocks = ((long long)n * (d / 4) + 255) / 256;
     const int grid = d_hidden ? (int)(blocks < 148 * 16 ? blocks : 148 * 16) : 148;
     const float* part = (const float*)(ws + L.dh);
     const long long head_n = (long long)vocab * d;
