@@ -614,6 +614,11 @@ __device__ __forceinline__ int target_of(const void* ids, int id_bytes, int i, i
   return t >= 0 && t < vocab ? (int)t : -1;
 }
 
+// Entries per block of the few-rows kernel: one block per SM of the B200, in
+// steps of 32 (tiles of 128 dealt round leave half of the SMs idle in the last
+// round: 50021 entries are 2.6 tiles an SM).
+__host__ __device__ inline int few_range(int v) { return ((v + 147) / 148 + 31) / 32 * 32; }
+
 template <int NT>
 struct Few {
   static constexpr int H_BYTES = NT * 128;
@@ -685,24 +690,27 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   const int kblocks = (p.d + BK - 1) / BK;
   const int products = n_products(p.planes, 1);
   const int iters = products * kblocks;
-  const int tiles = skip_cta || nv == 0 ? 0 : (p.vc + 127) / 128;
+  // the CTA's entries: as even as 32 rows (a box) allow
+  const int per = few_range(p.vc);
+  const int v0 = min((int)blockIdx.x * per, p.vc);
+  const int v1 = skip_cta || nv == 0 ? v0 : min(v0 + per, p.vc);
 
   if (warp == 0) {
     const bool issuer = elect_one();
     int stage = 0;
     uint32_t phase = 0, armed = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const int v = p.v0 + t * 128;
+    for (int t = v0; t < v1 && ok; t += 128) {
+      const int v = p.v0 + t, boxes = (min(v1 - t, 128) + 31) / 32;
       for (int kb = 0, q = 0; kb < kblocks;) {
         if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
         armed &= ~(1u << stage);
         uint8_t* sa = smem + stage * SM::STAGE;
         if (issuer) {
           const int ta = term_a(q, products), tb = term_b(q, products);
-          mbar_expect_tx(&full[stage], SM::STAGE);
-          tma_load_3d(&maps.b, &full[stage], sa, kb * BK, v, tb);
-          tma_load_3d(&maps.b, &full[stage], sa + BOX_BYTES, kb * BK, v + 64, tb);
+          mbar_expect_tx(&full[stage], boxes * (BOX_BYTES / 2) + SM::H_BYTES);
+          for (int h = 0; h < boxes; ++h)
+            tma_load_3d(&maps.b, &full[stage], sa + h * (BOX_BYTES / 2), kb * BK, v + 32 * h, tb);
           tma_load_3d(&maps.a, &full[stage], sa + 2 * BOX_BYTES, kb * BK, 0, ta);
         }
         armed |= 1u << stage;
@@ -729,7 +737,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     int stage = 0, buf = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    for (int t = v0; t < v1 && ok; t += 128) {
       for (int it = 0; it < iters && ok;) {
         if (!mbar_wait_warp(&tempty[buf], acc_phase ^ 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
@@ -774,8 +782,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         sum[i] = 0.f;
       }
     }
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const int v = t * 128 + quarter * 32 + lane;   // in the piece
+    for (int t = v0; t < v1 && ok; t += 128) {
+      const int v = t + quarter * 32 + lane;   // in the piece
       float acc[NT];
 #pragma unroll
       for (int i = 0; i < NT; ++i) acc[i] = 0.f;
@@ -802,7 +810,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         if (++buf == 2) { buf = 0; acc_phase ^= 1; }
       }
       if (!ok) break;
-      const bool in = v < p.vc;
+      const bool in = v < v1;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const float l = acc[i] * p.scale;
@@ -1235,8 +1243,7 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 int round_up(int a, int b) { return (a + b - 1) / b * b; }
 int div_up(int a, int b) { return (a + b - 1) / b; }
 
-// Blocks of the few-rows kernel: one per SM of the B200, a vocabulary tile of 128 each at least.
-int few_blocks(int v) { return div_up(v, 128) < 148 ? div_up(v, 128) : 148; }
+int few_blocks(int v) { return div_up(v, few_range(v)); }
 
 // Whether the loss of fp32 rows runs on plain multiply-adds (the rows have to
 // fit the shared memory, up to 3200 columns for 16 of them).
@@ -1368,6 +1375,11 @@ cudaError_t launch_f32_few(const LossParams& p, const void* hidden, const void* 
   return cudaGetLastError();
 }
 
+// The head as the few-rows kernel reads it: boxes of 32 entries.
+cudaError_t few_head_map(CUtensorMap* map, const void* head, int v, int d, int planes) {
+  return make_map(map, head, false, d, d, v, planes, BK, 32);
+}
+
 // Hidden rows as the few-rows kernel reads them: boxes of NT rows.
 cudaError_t few_map(CUtensorMap* map, const void* rows, int n, int d, int planes) {
   return make_map(map, rows, false, d, d, n, planes, BK, n <= 16 ? 16 : FEW_ROWS);
@@ -1466,7 +1478,7 @@ extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d
     } else {
       jp.blocks = few_blocks(vocab);
       e = few_map(&maps.a, hidden, n, d, 1);
-      if (e == cudaSuccess) e = load_map(&maps.b, head, d, d, vocab, 1);
+      if (e == cudaSuccess) e = few_head_map(&maps.b, head, vocab, d, 1);
       if (e == cudaSuccess) e = n <= 16 ? launch_few<LSE, 16>(maps, p, st) : launch_few<LSE, 64>(maps, p, st);
     }
     if (e == cudaSuccess) e = join(n, 0);
@@ -1474,8 +1486,9 @@ extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d
   }
   const void* w = nullptr;
   cudaError_t e = head_operand(L, ws, head, vocab, d, f32, &w, st);
-  if (e == cudaSuccess) e = load_map(&maps.b, w, d, d, vocab, L.planes);
   const bool few = n <= FEW_ROWS;   // up to 64 rows: bound by reading the head
+  if (e == cudaSuccess)
+    e = few ? few_head_map(&maps.b, w, vocab, d, L.planes) : load_map(&maps.b, w, d, d, vocab, L.planes);
   for (int r0 = 0; r0 < n && e == cudaSuccess; r0 += L.rows) {
     const int nr = n - r0 < L.rows ? n - r0 : L.rows;
     RowParams rp{};
@@ -1539,6 +1552,7 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
   p.want_dw = d_head != nullptr; p.want_dh = d_hidden != nullptr; p.dw_bf16 = !f32; p.k_split = L.k_split;
   const bool few = n <= FEW_ROWS;
   if (e == cudaSuccess && few) e = few_map(&mp.a, ws + L.rows_b, n, d, L.planes);
+  if (e == cudaSuccess && few) e = few_head_map(&mp.b, w, vocab, d, L.planes);
   const int pitch = round_up(L.vc, 64), mt = div_up(n, TILE), dt = div_up(d, TILE);
   for (int v0 = 0; v0 < vocab && e == cudaSuccess; v0 += L.vc) {
     p.v0 = v0;
