@@ -7,7 +7,7 @@
 // in the order of n, so the result does not depend on the schedule: no
 // floating-point atomics.  Two ways, by the number of tokens:
 //
-//   few tokens: a block owns 32 table rows and looks through all ids; one
+//   few tokens: a block owns up to 32 table rows and looks through all ids; one
 //     launch, nothing to sort.
 //   many tokens: a stable radix sort of (id, n) by 9 bits a pass (in one block
 //     up to 8192 tokens); then the
@@ -64,7 +64,8 @@ __global__ void __launch_bounds__(256) embed_kernel(const void* ids, int id_byte
 // one row, which one group of threads adds up: 870 tokens with a few frequent
 // ids (table 1323 x 1168) took 148 us here and 25 us sorted; 67 tokens 6 us.
 constexpr int SCAN_MAX = 128;
-constexpr int SCAN_ROWS = 32;       // table rows of a block
+// Table rows of a block: enough blocks for the device where the table is small.
+int scan_rows(int vocab) { return vocab >= 32 * 592 ? 32 : (vocab >= 592 ? vocab / 592 : 1); }
 
 template <typename T>
 __device__ __forceinline__ void write_row(T* dst, const float* acc, float scale, bool accumulate) {
@@ -86,19 +87,19 @@ __device__ __forceinline__ void write_row(T* dst, const float* acc, float scale,
 template <typename T>
 __global__ void __launch_bounds__(256) embed_grad_scan_kernel(const void* ids, int id_bytes, const T* d_out,
                                                               float scale, T* d_table, int n, int vocab, int d,
-                                                              int accumulate) {
+                                                              int accumulate, int block_rows) {
   __shared__ unsigned char s_n[SCAN_MAX];    // tokens of the block's rows, in order
   __shared__ unsigned char s_row[SCAN_MAX];
   __shared__ int s_warp[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int v0 = blockIdx.x * SCAN_ROWS;
+  const int v0 = blockIdx.x * block_rows;
   int found = 0;
   for (int b = 0; b < n; b += 256) {
     const int i = b + threadIdx.x;
     int r = -1;
     if (i < n) {
       const long long id = load_id(ids, id_bytes, i);
-      if (id >= v0 && id < v0 + SCAN_ROWS && id < vocab) r = (int)(id - v0);
+      if (id >= v0 && id < v0 + block_rows && id < vocab) r = (int)(id - v0);
     }
     const unsigned mask = __ballot_sync(0xffffffffu, r >= 0);
     if (lane == 0) s_warp[warp] = __popc(mask);
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(256) embed_grad_scan_kernel(const void* ids, i
     }
     __syncthreads();
   }
-  const int rows = min(SCAN_ROWS, vocab - v0), vecs = d / 8;
+  const int rows = min(block_rows, vocab - v0), vecs = d / 8;
   for (int k = threadIdx.x; k < rows * vecs; k += 256) {
     const int r = k / vecs, c = (k - r * vecs) * 8;
     float acc[8];
@@ -569,8 +570,9 @@ template <typename T>
 cudaError_t embed_grad(int n, int vocab, int d, const void* ids, int id_bytes, const T* d_out, float scale,
                        T* d_table, int accumulate, char* ws, cudaStream_t st) {
   if (n <= SCAN_MAX) {
-    embed_grad_scan_kernel<T><<<(vocab + SCAN_ROWS - 1) / SCAN_ROWS, 256, 0, st>>>(ids, id_bytes, d_out, scale, d_table,
-                                                                                 n, vocab, d, accumulate);
+    const int rows = scan_rows(vocab);
+    embed_grad_scan_kernel<T><<<(vocab + rows - 1) / rows, 256, 0, st>>>(ids, id_bytes, d_out, scale, d_table, n, vocab,
+                                                                        d, accumulate, rows);
     return cudaGetLastError();
   }
   const GradLayout L(n, d);

@@ -72,14 +72,13 @@ struct Smem {
 
 constexpr int ROW_GROUP = 32;          // row tiles that share a vocabulary tile before the next one
 constexpr int LSE_CHUNK = 8;           // k-blocks per accumulator of the loss's logits (K = 512)
-constexpr int FEW_CHUNK = 2;           // ... of few rows' logits, where it costs nothing (K = 128)
 constexpr int F32_CHUNK = 4;           // ... of everything that fp32 operands give (K = 256)
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct LossParams {
   int n_rows, d, vocab;
+  int two_terms;              // GRAD, few bf16 rows: the second terms of P stand as further rows, this far behind
   int planes;                 // 1: bf16 operands; 3: fp32 operands as three bf16 terms
-  int p_planes;               // terms of P: 1 or 2 beside bf16 operands, 3 beside fp32 ones
   int v0, vc;                 // vocabulary piece
   int chunk;                  // k-blocks per accumulator
   float scale;
@@ -89,7 +88,8 @@ struct LossParams {
   float2* part; int part_pitch; float* target_logit;
   // PROB
   const float* lse; const float* g;
-  bf16* p_out; int p_trans;   // few rows: P is kept transposed, [term][entry][NT], each thread writing its entry
+  bf16* p_out; int p_trans;   // few rows: P is kept transposed, each thread writing its entry: [term][entry][NT], or
+                              // [entry][term][NT] beside bf16 operands
   // few rows, LSE: rows in their own order, targets as the caller gave them
   const void* ids; int id_bytes; unsigned* block_err;
   // GRAD
@@ -103,12 +103,11 @@ struct LossMaps {
   CUtensorMap out0, out1;     // PROB: P; GRAD: dW, dH partial sums
 };
 
-// Products of a tile and the terms that product q multiplies (smallest products
-// first): six with fp32 operands; with bf16 ones as many as the first operand
-// (P) has terms.
-__device__ __forceinline__ int n_products(int planes, int a_terms) { return planes == 3 ? 6 : a_terms; }
+// Products of a tile, and the terms that product q of fp32 operands multiplies
+// (smallest products first).
+__device__ __forceinline__ int n_products(int planes) { return planes == 3 ? 6 : 1; }
 __device__ __forceinline__ int term_a(int q, int products) {
-  return products == 6 ? (0x021010 >> (4 * (5 - q))) & 15 : products - 1 - q;
+  return products == 6 ? (0x021010 >> (4 * (5 - q))) & 15 : 0;
 }
 __device__ __forceinline__ int term_b(int q, int products) {
   return products == 6 ? (0x201100 >> (4 * (5 - q))) & 15 : 0;
@@ -343,9 +342,9 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (wrow0 >= p.n_rows || pc + 64 * h >= p.vc) continue;   // nothing of this box is in P
-      for (int t = 0; t < p.p_planes; ++t) {
+      for (int t = 0; t < p.planes; ++t) {
         emit_bf16x64(&maps.out0, slot(), lane, sums + 32 * h, pc + 64 * h, wrow0, t);
-        if (t + 1 < p.p_planes) {   // what the term just written leaves of the value
+        if (t + 1 < p.planes) {   // what the term just written leaves of the value
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float2 hi = __bfloat1622float2(__float22bfloat162_rn(sums[32 * h + i]));
@@ -441,9 +440,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   const bool skip = ld_cluster_u32(mapa_shared(smem_u32(skip_word), 0)) != 0;
 
-  const int nv = *p.n_valid;
+  const int nv = ROLE == GRAD && p.two_terms ? 2 * p.two_terms : *p.n_valid;
   const Jobs<ROLE> jobs(p, nv);
-  const int products = n_products(p.planes, ROLE == GRAD ? p.p_planes : 1);
+  const int products = n_products(p.planes);
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
 
   if (warp < 4) {
@@ -608,6 +607,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 // of head per SM in the pair kernel), and the products cost next to nothing.
 // Thread = vocabulary entry; LSE keeps a running (max, sum) per hidden row in
 // registers over all tiles of the CTA and joins the 32 lanes at the end.
+// One more logit in a running (max, sum of exponentials); one exponential: that
+// of the smaller relative to the larger.  (Equal infinities count as 1: where
+// the maximum stays -inf the sum is not used.)
+__device__ __forceinline__ void add_logit(float l, float& m, float& sum) {
+  const float d = l == m ? 0.f : l - m;
+  const float e = ex2(-fabsf(d) * LOG2E);
+  sum = l > m ? fmaf(sum, e, 1.f) : sum + e;
+  m = fmaxf(m, l);
+}
+
+// Two running (max, sum) as one.
+__device__ __forceinline__ void merge(float& m, float& sum, float om, float os) {
+  const float nm = fmaxf(m, om), base = nm == -INFINITY ? 0.f : nm;
+  sum = sum * ex2((m - base) * LOG2E) + os * ex2((om - base) * LOG2E);
+  m = nm;
+}
+
 // A row's target, -1 where it has none.
 __device__ __forceinline__ int target_of(const void* ids, int id_bytes, int i, int vocab) {
   const long long t = load_id(ids, id_bytes, i);
@@ -688,12 +704,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int kblocks = (p.d + BK - 1) / BK;
-  const int products = n_products(p.planes, 1);
+  const int products = n_products(p.planes);
   const int iters = products * kblocks;
   // the CTA's entries: as even as 32 rows (a box) allow
   const int per = few_range(p.vc);
   const int v0 = min((int)blockIdx.x * per, p.vc);
-  const int v1 = skip_cta || nv == 0 ? v0 : min(v0 + per, p.vc);
+  const int v1 = skip_cta || (ROLE == LSE && nv == 0) ? v0 : min(v0 + per, p.vc);   // PROB: P is read in any case
 
   if (warp == 0) {
     const bool issuer = elect_one();
@@ -816,11 +832,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         const float l = acc[i] * p.scale;
         const bool hit = s_target[i] == p.v0 + v;
         if constexpr (ROLE == LSE) {
-          const float x = in ? l : -INFINITY;
-          const float nm = fmaxf(m[i], x);
-          const float base = nm == -INFINITY ? 0.f : nm;
-          sum[i] = sum[i] * ex2((m[i] - base) * LOG2E) + ex2((x - base) * LOG2E);
-          m[i] = nm;
+          if (in) add_logit(l, m[i], sum[i]);
           if (hit && in) p.target_logit[i] = l;
         } else {
           const float g = s_g[i];
@@ -830,8 +842,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         }
       }
       if constexpr (ROLE == PROB) {
-        for (int q = 0; q < p.p_planes; ++q) {
-          bf16* dst = p.p_out + ((long long)q * p.vc + v) * NT;
+        // fp32 operands: a plane a term; bf16: two terms side by side
+        const int terms = p.planes == 3 ? 3 : 2;
+        for (int q = 0; q < terms; ++q) {
+          bf16* dst = p.p_out + (p.planes == 3 ? ((long long)q * p.vc + v) * NT : ((long long)v * 2 + q) * NT);
 #pragma unroll
           for (int i = 0; i < NT; i += 8) {
             Vec8<bf16> y;
@@ -846,18 +860,32 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       }
     }
     if constexpr (ROLE == LSE) {
+      // over the lanes: at each step a lane keeps half of its rows (those whose
+      // number has the lane's bit), so that NT rows take about NT merges, not 5 NT
+      constexpr int W = NT < 32 ? NT : 32;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
+      for (int o = W / 2, n = NT; o; o >>= 1, n >>= 1) {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          const float om = __shfl_xor_sync(0xffffffffu, m[i], o), os = __shfl_xor_sync(0xffffffffu, sum[i], o);
-          const float nm = fmaxf(m[i], om);
-          const float base = nm == -INFINITY ? 0.f : nm;
-          sum[i] = sum[i] * ex2((m[i] - base) * LOG2E) + os * ex2((om - base) * LOG2E);
-          m[i] = nm;
+        for (int i = 0; i < NT / 2; ++i) {
+          if (i < n / 2) {
+            const int at = i / o * 2 * o + i % o;
+            const bool up = lane & o;
+            const float om = __shfl_xor_sync(0xffffffffu, up ? m[at] : m[at + o], o);
+            const float os = __shfl_xor_sync(0xffffffffu, up ? sum[at] : sum[at + o], o);
+            m[i] = up ? m[at + o] : m[at];
+            sum[i] = up ? sum[at + o] : sum[at];
+            merge(m[i], sum[i], om, os);
+          }
         }
-        if (lane == 0 && i < p.part_pitch)
-          p.part[(long long)(blockIdx.x * 4 + quarter) * p.part_pitch + i] = make_float2(m[i], sum[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < NT / W; ++i) {   // row 32 i + lane (16 rows: lane mod 16)
+#pragma unroll
+        for (int o = 16; o >= W; o >>= 1)
+          merge(m[i], sum[i], __shfl_xor_sync(0xffffffffu, m[i], o), __shfl_xor_sync(0xffffffffu, sum[i], o));
+        const int row = i * W + lane;
+        if (lane < W && row < p.part_pitch)
+          p.part[(long long)(blockIdx.x * 4 + quarter) * p.part_pitch + row] = make_float2(m[i], sum[i]);
       }
     }
   }
@@ -962,9 +990,7 @@ __global__ void __launch_bounds__(F32_FEW_THREADS, 1) token_loss_f32_few_kernel(
       const int i = 32 * u + lane, entry = 4 * g + i / NT;
       if (i < N && entry < p.vocab) {
         const float l = v[u] * p.scale;
-        const float nm = fmaxf(m, l), base = nm == -INFINITY ? 0.f : nm;
-        sum = sum * ex2((m - base) * LOG2E) + ex2((l - base) * LOG2E);
-        m = nm;
+        add_logit(l, m, sum);
         if (entry == target) p.target_logit[row] = l;
       }
     }
@@ -972,10 +998,7 @@ __global__ void __launch_bounds__(F32_FEW_THREADS, 1) token_loss_f32_few_kernel(
   // lanes of the same row
 #pragma unroll
   for (int o = 16; o >= NT; o >>= 1) {
-    const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, sum, o);
-    const float nm = fmaxf(m, om), base = nm == -INFINITY ? 0.f : nm;
-    sum = sum * ex2((m - base) * LOG2E) + os * ex2((om - base) * LOG2E);
-    m = nm;
+    merge(m, sum, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o));
   }
   if (lane < NT && row < p.n_rows)
     p.part[(long long)(blockIdx.x * (F32_FEW_THREADS / 32) + warp) * p.part_pitch + row] = make_float2(m, sum);
@@ -989,6 +1012,7 @@ __global__ void __launch_bounds__(F32_FEW_THREADS, 1) token_loss_f32_few_kernel(
 struct RowParams {
   int n, d, vocab, rows_per_block;
   int clear_err;
+  int twice;                  // few bf16 rows: rows 0 .. twice-1, zeros behind the last, and the same again
   const void* targets; int target_bytes;
   const void* hidden;
   bf16* rows;                 // [planes][n][d]
@@ -1016,14 +1040,15 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
   __shared__ int s_slot[64];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r0 = blockIdx.x * p.rows_per_block;
-  const int nr = min(p.rows_per_block, p.n - r0);
+  const int rows = max(p.n, p.twice), nr = min(p.rows_per_block, rows - r0);
   auto valid = [&](int i) {
+    if (i >= p.n) return false;
     const long long t = load_id(p.targets, p.target_bytes, i);
     return t >= 0 && t < p.vocab;
   };
   int before = 0;
   float gm = 0.f;
-  const int scan = p.d_loss ? p.n : r0;
+  const int scan = p.d_loss ? p.n : min(r0, p.n);
   for (int i = threadIdx.x; i < scan; i += 256) {
     const bool ok = valid(i);
     if (ok && i < r0) ++before;
@@ -1060,8 +1085,11 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
       const unsigned mask = __ballot_sync(0xffffffffu, ok);
       const int vb = seen + __popc(mask & ((1u << lane) - 1));   // rows with a target before row i
       if (here) {
-        const int at = ok ? vb : p.n - 1 - (i - vb);
+        const int at = ok ? vb : (i < p.n ? p.n - 1 - (i - vb) : i);
         s_slot[b + lane] = ok ? at : ~at;
+      }
+      if (here && i < p.n) {
+        const int at = ok ? vb : p.n - 1 - (i - vb);
         p.perm[at] = i;
         p.target[at] = ok ? (int)load_id(p.targets, p.target_bytes, i) : -1;
         if (p.d_loss) {
@@ -1075,7 +1103,7 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
       }
       seen += __popc(mask);
     }
-    if (r0 + nr == p.n && lane == 0) *p.n_valid = seen;
+    if (r0 + nr == rows && lane == 0) *p.n_valid = seen;
   }
   __syncthreads();
   const int vecs = p.d / 8;   // 8 elements per step, four steps in flight
@@ -1098,6 +1126,7 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
       bf16* dst = p.rows + (long long)at * p.d + c;
       if constexpr (sizeof(T) == 2) {
         x[u].store(dst);
+        if (p.twice) x[u].store(dst + (long long)p.twice * p.d);
       } else {
         float f[8];
         x[u].get(f);
@@ -1149,12 +1178,6 @@ __global__ void __launch_bounds__(1024) join_lse_kernel(const JoinParams p) {
     bad = *p.err != 0;
   }
   float m = -INFINITY, sum = 0.f;
-  auto add = [&](float2 o) {
-    const float nm = fmaxf(m, o.x);
-    const float base = nm == -INFINITY ? 0.f : nm;
-    sum = sum * ex2((m - base) * LOG2E) + o.y * ex2((o.x - base) * LOG2E);
-    m = nm;
-  };
   if (in) {
     for (int i0 = y; i0 < p.n_parts; i0 += 8 * ny) {   // eight at a time: one running maximum for all
       float2 o[8];
@@ -1176,7 +1199,7 @@ __global__ void __launch_bounds__(1024) join_lse_kernel(const JoinParams p) {
   __syncthreads();
   for (int h = ny / 2; h; h >>= 1) {
     if (y < h) {
-      add(s[threadIdx.x + h * p.rb]);
+      merge(m, sum, s[threadIdx.x + h * p.rb].x, s[threadIdx.x + h * p.rb].y);
       s[threadIdx.x] = make_float2(m, sum);
     }
     __syncthreads();
@@ -1193,11 +1216,13 @@ __global__ void __launch_bounds__(1024) join_lse_kernel(const JoinParams p) {
   }
 }
 
-// dH rows back in their order: the splits' partial sums added in order, times
+// dH rows back in their order: the splits' partial sums (of `rows` rows; with
+// two terms of P those of both) added in order, times
 // the weights' common factor.  After a wait that ran out, NaN there and in the
 // head's gradient.  Either may be null.
 template <typename T>
-__global__ void __launch_bounds__(256) join_rows_kernel(const float* part, int splits, int n, int d, const int* perm,
+__global__ void __launch_bounds__(256) join_rows_kernel(const float* part, int splits, int rows, int two_terms, int n,
+                                                        int d, const int* perm,
                                                         const int* n_valid, const float* g_max, float scale,
                                                         const unsigned* err, T* out, T* head, long long head_n) {
   const int nv = *n_valid;
@@ -1209,7 +1234,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const float* part, int s
   if (!out) return;
   const float f = *g_max * scale;
   const int vecs = d / 4;
-  const long long total = (long long)n * vecs, plane = (long long)n * d;
+  const long long total = (long long)n * vecs, plane = (long long)rows * d;
   for (long long k = (long long)blockIdx.x * 256 + threadIdx.x; k < total; k += (long long)gridDim.x * 256) {
     const int r = (int)(k / vecs), c = (int)(k - (long long)r * vecs) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1219,6 +1244,10 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const float* part, int s
       for (int s = 0; s < splits; ++s) {
         const float4 a = *reinterpret_cast<const float4*>(part + s * plane + (long long)r * d + c);
         v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+        if (two_terms) {
+          const float4 b = *reinterpret_cast<const float4*>(part + s * plane + (long long)(r + two_terms) * d + c);
+          v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
+        }
       }
       v.x *= f; v.y *= f; v.z *= f; v.w *= f;
     }
@@ -1252,21 +1281,26 @@ bool f32_few(bool f32, int n, int d, bool grad) {
   return f32 && !grad && n <= F32_FEW_ROWS && (size_t)f32_few_rows(n) * d * 4 <= 200 * 1024;
 }
 
+// Columns of the few-rows kernel's products.
+int few_cols(int n) { return n <= 16 ? 16 : FEW_ROWS; }
+
 // Workspace of one call, laid out in order.
 struct Layout {
-  int planes, p_planes, rows, pieces, vc, splits, k_split, n_parts;
+  int planes, rows, g_rows, two_terms, pieces, vc, splits, k_split, n_parts;
   size_t block_err, n_valid, g_max, rows_b, perm, target, g, lse, tlogit, part, head, p, dh, total;
   Layout(int n, int v, int d, bool f32, bool grad) {
     planes = f32 ? 3 : 1;
-    // P beside bf16 operands: one bf16 term; two for few rows, where the products
-    // are not what bounds the gradient and few roundings average out
-    p_planes = f32 ? 3 : (n <= 128 ? 2 : 1);
+    // P beside bf16 operands is one bf16 term; for few rows two (few roundings do
+    // not average out, and the products are not what bounds the gradient): the
+    // second terms stand as further rows of P, beside the same hidden rows again
+    two_terms = grad && !f32 && n <= FEW_ROWS ? few_cols(n) : 0;
+    g_rows = two_terms ? 2 * two_terms : n;
     const bool simt = f32_few(f32, n, d, grad);
     rows = grad ? n : (n < LOSS_ROWS ? n : LOSS_ROWS);
     n_parts = simt ? 148 * (F32_FEW_THREADS / 32) : (n <= FEW_ROWS ? 4 * few_blocks(v) : 2 * div_up(v, TILE));
     vc = v; pieces = 1; splits = k_split = 0;
     if (grad) {
-      long long w = P_BYTES / ((long long)n * 2 * p_planes) / TILE * TILE;
+      long long w = P_BYTES / ((long long)g_rows * 2 * planes) / TILE * TILE;
       if (w < TILE) w = TILE;
       if (w < v) {
         pieces = div_up(v, (int)w);
@@ -1275,8 +1309,8 @@ struct Layout {
       }
       // dH tiles contract over the piece in splits, so that a launch has about four
       // tiles of equal work per CTA pair; of 256 to 8192 columns each
-      const long long mt = div_up(n, TILE), dt = div_up(d, TILE), nt = div_up(vc, TILE);
-      const long long blocks = dt * (mt * div_up(vc, BK) + nt * div_up(n, BK));
+      const long long mt = div_up(g_rows, TILE), dt = div_up(d, TILE), nt = div_up(vc, TILE);
+      const long long blocks = dt * (mt * div_up(vc, BK) + nt * div_up(g_rows, BK));
       const long long want = blocks / (4 * 74);
       const int ks = BK * (int)(want < 4 ? 4 : (want > 128 ? 128 : want));
       splits = div_up(vc, ks);
@@ -1288,7 +1322,7 @@ struct Layout {
     block_err = take(148 * 4);
     n_valid = take(4);
     g_max = take(4);
-    rows_b = take((size_t)planes * rows * d * 2);
+    rows_b = take((size_t)planes * (grad ? g_rows : rows) * d * 2);
     perm = take((size_t)rows * 4);
     target = take((size_t)rows * 4);
     g = take(grad ? (size_t)rows * 4 : 0);
@@ -1296,8 +1330,8 @@ struct Layout {
     tlogit = take(grad ? 0 : (size_t)rows * 4);
     part = take(grad ? 0 : (size_t)n_parts * rows * 8);
     head = take(f32 && !simt ? (size_t)3 * v * d * 2 : 0);
-    p = take(grad ? (size_t)p_planes * (n <= 16 ? 16 : (n <= FEW_ROWS ? FEW_ROWS : n)) * round_up(vc, 64) * 2 : 0);
-    dh = take(grad ? (size_t)splits * n * d * 4 : 0);
+    p = take(grad ? (size_t)planes * (two_terms ? g_rows : (n <= FEW_ROWS ? few_cols(n) : n)) * round_up(vc, 64) * 2 : 0);
+    dh = take(grad ? (size_t)splits * g_rows * d * 4 : 0);
     total = o;
   }
 };
@@ -1375,6 +1409,10 @@ cudaError_t launch_f32_few(const LossParams& p, const void* hidden, const void* 
   return cudaGetLastError();
 }
 
+// k-blocks per accumulator of few rows' logits: short ones cost nothing there
+// (K = 128 or 256).
+int few_chunk(int n) { return n <= 16 ? 2 : 4; }
+
 // The head as the few-rows kernel reads it: boxes of 32 entries.
 cudaError_t few_head_map(CUtensorMap* map, const void* head, int v, int d, int planes) {
   return make_map(map, head, false, d, d, v, planes, BK, 32);
@@ -1398,7 +1436,7 @@ cudaError_t launch_products(const LossMaps& maps, const LossParams& p, long long
 cudaError_t launch_order_rows(RowParams rp, bool f32, cudaStream_t st) {
   // blocks scan the targets before them: few rows each while that is cheap
   rp.rows_per_block = rp.n <= 2048 ? 4 : (rp.n <= 16384 ? 16 : 64);
-  const int grid = div_up(rp.n, rp.rows_per_block);
+  const int grid = div_up(rp.n > rp.twice ? rp.n : rp.twice, rp.rows_per_block);
   if (f32) order_rows_kernel<float><<<grid, 256, 0, st>>>(rp);
   else order_rows_kernel<bf16><<<grid, 256, 0, st>>>(rp);
   return cudaGetLastError();
@@ -1470,7 +1508,7 @@ extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d
     p.id_bytes = jp.id_bytes = target_bytes;
     p.block_err = (unsigned*)(ws + L.block_err);
     jp.block_err = p.block_err;
-    p.chunk = FEW_CHUNK;
+    p.chunk = few_chunk(n);
     cudaError_t e;
     if (simt) {
       jp.blocks = 148;
@@ -1506,7 +1544,7 @@ extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d
     p.n_valid = jp.n_valid = rp.n_valid;
     p.target = rp.target;
     jp.perm = rp.perm;
-    p.chunk = few ? FEW_CHUNK : (f32 ? F32_CHUNK : LSE_CHUNK);
+    p.chunk = few ? few_chunk(n) : (f32 ? F32_CHUNK : LSE_CHUNK);
     if (few) e = nr <= 16 ? launch_few<LSE, 16>(maps, p, st) : launch_few<LSE, 64>(maps, p, st);
     else e = launch_products<LSE>(maps, p, (long long)div_up(nr, TILE) * div_up(vocab, TILE), st);
     if (e == cudaSuccess) e = join(nr, r0);
@@ -1536,33 +1574,34 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
   rp.targets = targets; rp.target_bytes = target_bytes; rp.hidden = hidden;
   rp.rows = (bf16*)(ws + L.rows_b); rp.perm = (int*)(ws + L.perm); rp.target = (int*)(ws + L.target);
   rp.n_valid = (int*)(ws + L.n_valid); rp.err = (unsigned*)ws;
+  rp.twice = L.two_terms;
   rp.d_loss = d_loss; rp.lse_in = lse; rp.g = (float*)(ws + L.g); rp.lse = (float*)(ws + L.lse);
   rp.g_max = (float*)(ws + L.g_max);
   if (e == cudaSuccess) e = launch_order_rows(rp, f32, st);
   LossMaps mp{}, mg{};   // PROB, GRAD
-  if (e == cudaSuccess) e = load_map(&mp.a, ws + L.rows_b, d, d, n, L.planes);
+  if (e == cudaSuccess) e = load_map(&mp.a, ws + L.rows_b, d, d, L.g_rows, L.planes);
   if (e == cudaSuccess) e = load_map(&mp.b, w, d, d, vocab, L.planes);
   mg.b = mp.b;
   mg.c = mp.a;
   if (e == cudaSuccess && d_head) e = make_map(&mg.out0, d_head, f32, d, d, vocab, 1, f32 ? 32 : 64, 32);
-  if (e == cudaSuccess && d_hidden) e = make_map(&mg.out1, ws + L.dh, true, d, d, n, L.splits, 32, 32);
+  if (e == cudaSuccess && d_hidden) e = make_map(&mg.out1, ws + L.dh, true, d, d, L.g_rows, L.splits, 32, 32);
   LossParams p{};
-  p.n_rows = n; p.d = d; p.vocab = vocab; p.planes = L.planes; p.p_planes = L.p_planes; p.scale = scale;
+  p.n_rows = n; p.d = d; p.vocab = vocab; p.planes = L.planes; p.scale = scale;
   p.n_valid = rp.n_valid; p.target = rp.target; p.lse = rp.lse; p.g = rp.g; p.g_max = rp.g_max; p.err = rp.err;
   p.want_dw = d_head != nullptr; p.want_dh = d_hidden != nullptr; p.dw_bf16 = !f32; p.k_split = L.k_split;
   const bool few = n <= FEW_ROWS;
   if (e == cudaSuccess && few) e = few_map(&mp.a, ws + L.rows_b, n, d, L.planes);
   if (e == cudaSuccess && few) e = few_head_map(&mp.b, w, vocab, d, L.planes);
-  const int pitch = round_up(L.vc, 64), mt = div_up(n, TILE), dt = div_up(d, TILE);
+  const int pitch = round_up(L.vc, 64), mt = div_up(L.g_rows, TILE), dt = div_up(d, TILE);
   for (int v0 = 0; v0 < vocab && e == cudaSuccess; v0 += L.vc) {
     p.v0 = v0;
     p.vc = vocab - v0 < L.vc ? vocab - v0 : L.vc;
     p.splits = div_up(p.vc, L.k_split);
     p.dh_add = v0 > 0;
-    const int nt16 = n <= 16 ? 16 : FEW_ROWS;
-    if (few) e = load_map(&mg.a, ws + L.p, n, nt16, p.vc, L.p_planes);
-    else e = load_map(&mg.a, ws + L.p, p.vc, pitch, n, L.p_planes);
-    if (e == cudaSuccess && !few) e = make_map(&mp.out0, ws + L.p, false, p.vc, pitch, n, L.p_planes, 64, 32);
+    if (L.two_terms) e = load_map(&mg.a, ws + L.p, L.g_rows, L.g_rows, p.vc, 1);
+    else if (few) e = load_map(&mg.a, ws + L.p, n, few_cols(n), p.vc, L.planes);
+    else e = load_map(&mg.a, ws + L.p, p.vc, pitch, n, L.planes);
+    if (e == cudaSuccess && !few) e = make_map(&mp.out0, ws + L.p, false, p.vc, pitch, n, L.planes, 64, 32);
     p.chunk = f32 ? F32_CHUNK : 1 << 30;
     const int nt = div_up(p.vc, TILE);
     p.p_out = (bf16*)(ws + L.p);
@@ -1570,8 +1609,11 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     if (e == cudaSuccess)
       e = !few ? launch_products<PROB>(mp, p, (long long)mt * nt, st)
                : (n <= 16 ? launch_few<PROB, 16>(mp, p, st) : launch_few<PROB, 64>(mp, p, st));
+    LossParams pg = p;
+    pg.n_rows = L.g_rows;
+    pg.two_terms = L.two_terms;
     const long long jobs = (p.want_dw ? (long long)nt * dt : 0) + (p.want_dh ? (long long)mt * dt * p.splits : 0);
-    if (e == cudaSuccess) e = launch_products<GRAD>(mg, p, jobs, st);
+    if (e == cudaSuccess) e = launch_products<GRAD>(mg, pg, jobs, st);
   }
   if (e == cudaSuccess) {
     const long long blocks = ((long long)n * (d / 4) + 255) / 256;
@@ -1579,10 +1621,10 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     const float* part = (const float*)(ws + L.dh);
     const long long head_n = (long long)vocab * d;
     if (f32)
-      join_rows_kernel<float><<<grid, 256, 0, st>>>(part, L.splits, n, d, rp.perm, rp.n_valid, rp.g_max, scale, rp.err,
+      join_rows_kernel<float><<<grid, 256, 0, st>>>(part, L.splits, L.g_rows, L.two_terms, n, d, rp.perm, rp.n_valid, rp.g_max, scale, rp.err,
                                                     (float*)d_hidden, (float*)d_head, head_n);
     else
-      join_rows_kernel<bf16><<<grid, 256, 0, st>>>(part, L.splits, n, d, rp.perm, rp.n_valid, rp.g_max, scale, rp.err,
+      join_rows_kernel<bf16><<<grid, 256, 0, st>>>(part, L.splits, L.g_rows, L.two_terms, n, d, rp.perm, rp.n_valid, rp.g_max, scale, rp.err,
                                                    (bf16*)d_hidden, (bf16*)d_head, head_n);
     e = cudaGetLastError();
   }
