@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(1024, 1) sort_block_kernel(const void* ids, in
     key[s] = k < per_warp && i < n ? sort_key(ids, id_bytes, nullptr, i, vocab) : -1;
   }
   if (threadIdx.x == 0) *clear = 0;
-  for (int shift = 0; shift == 0 || (vocab >> shift) != 0; shift += RADIX_BITS) {
+  for (int shift = 0; shift < 31 && (shift == 0 || (vocab >> shift) != 0); shift += RADIX_BITS) {
     for (int i = threadIdx.x; i < BLOCK_SORT_WARPS * RADIX / 2; i += 1024) reinterpret_cast<int*>(cnt)[i] = 0;
     __syncthreads();
     int rank[BLOCK_SORT_STEPS];
@@ -587,7 +587,7 @@ cudaError_t embed_grad(int n, int vocab, int d, const void* ids, int id_bytes, c
     sort_block_kernel<<<1, 1024, BLOCK_SORT_SMEM, st>>>(ids, id_bytes, n, vocab, (int*)keys, (int*)pos, n_open);
   } else {
     int to = 0;
-    for (int shift = 0; shift == 0 || (vocab >> shift) != 0; shift += RADIX_BITS) {   // keys are 0 .. vocab
+    for (int shift = 0; shift < 31 && (shift == 0 || (vocab >> shift) != 0); shift += RADIX_BITS) {   // keys are 0 .. vocab
       sort_count_kernel<<<L.tiles, 256, 0, st>>>(ids, id_bytes, keys, n, vocab, shift, hist, shift ? nullptr : n_open);
       int* ok = (int*)(ws + L.keys[to]);
       int* op = (int*)(ws + L.pos[to]);

@@ -72,6 +72,7 @@ struct Smem {
 
 constexpr int ROW_GROUP = 32;          // row tiles that share a vocabulary tile before the next one
 constexpr int LSE_CHUNK = 8;           // k-blocks per accumulator of the loss's logits (K = 512)
+constexpr int WHOLE_CHUNK = 1 << 16;   // ... of what is rounded to bf16 (K = 4 M: well inside the bounded waits)
 constexpr int F32_CHUNK = 4;           // ... of everything that fp32 operands give (K = 256)
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -1017,6 +1018,7 @@ struct RowParams {
   const void* hidden;
   bf16* rows;                 // [planes][n][d]
   int* perm; int* target; int* n_valid;
+  const int2* counts;         // many rows: rows with a target and the largest |weight| (its bits) of every 1024 rows
   // gradient: weights divided by the largest magnitude (so that a weight that
   // is the same for all rows leaves P at exact multiples), lse gathered
   const float* d_loss; const float* lse_in; float* g; float* lse; float* g_max;
@@ -1026,11 +1028,33 @@ struct RowParams {
 };
 
 __device__ __forceinline__ void split3(float x, bf16& hi, bf16& mid, bf16& lo) {
-  hi = __float2bfloat16_rn(x);
+  hi = __float2bfloat16_rz(x);   // toward zero: the largest fp32 numbers stay finite
   const float r = x - __bfloat162float(hi);
   mid = __float2bfloat16_rn(r);
   lo = __float2bfloat16_rn(r - __bfloat162float(mid));
-  if (!isfinite(__bfloat162float(hi))) mid = lo = __float2bfloat16_rn(0.f);   // inf - inf would be NaN
+  if (!isfinite(x)) mid = lo = __float2bfloat16_rn(0.f);   // inf - inf would be NaN
+}
+
+__device__ __forceinline__ float max_or_nan(float a, float b) { return (b > a || b != b) ? b : a; }   // keeps a NaN of b
+
+// counts[k]: rows with a target among 1024 k .. 1024 k + 1023, and their largest
+// |weight|.  Without it every block of order_rows looks through all rows, which
+// is cheap up to some 10^4 of them only.
+constexpr int COUNT_ROWS = 1024;
+__global__ void __launch_bounds__(COUNT_ROWS) count_rows_kernel(const RowParams p, int2* counts) {
+  __shared__ float s_max[32];
+  const int i = blockIdx.x * COUNT_ROWS + threadIdx.x;
+  const bool ok = i < p.n && target_of(p.targets, p.target_bytes, i, p.vocab) >= 0;
+  float gm = ok ? fabsf(p.d_loss[i]) : 0.f;
+  const int count = __syncthreads_count(ok);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) gm = max_or_nan(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = gm;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 32; ++w) gm = max_or_nan(gm, s_max[w]);
+    counts[blockIdx.x] = make_int2(count, __float_as_int(gm));
+  }
 }
 
 template <typename T>
@@ -1041,27 +1065,29 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r0 = blockIdx.x * p.rows_per_block;
   const int rows = max(p.n, p.twice), nr = min(p.rows_per_block, rows - r0);
-  auto valid = [&](int i) {
-    if (i >= p.n) return false;
-    const long long t = load_id(p.targets, p.target_bytes, i);
-    return t >= 0 && t < p.vocab;
-  };
+  auto valid = [&](int i) { return i < p.n && target_of(p.targets, p.target_bytes, i, p.vocab) >= 0; };
   int before = 0;
   float gm = 0.f;
-  const int scan = p.d_loss ? p.n : min(r0, p.n);
-  for (int i = threadIdx.x; i < scan; i += 256) {
-    const bool ok = valid(i);
-    if (ok && i < r0) ++before;
-    if (ok && p.d_loss) {
-      const float g = fabsf(p.d_loss[i]);
-      gm = (g > gm || g != g) ? g : gm;   // keeps a NaN
+  if (p.counts) {
+    const int here = r0 / COUNT_ROWS;
+    for (int k = threadIdx.x; k < (p.n + COUNT_ROWS - 1) / COUNT_ROWS; k += 256) {
+      const int2 c = p.counts[k];
+      if (k < here) before += c.x;
+      gm = max_or_nan(gm, __int_as_float(c.y));
+    }
+    for (int i = here * COUNT_ROWS + threadIdx.x; i < r0; i += 256) before += valid(i);
+  } else {
+    const int scan = p.d_loss ? p.n : min(r0, p.n);
+    for (int i = threadIdx.x; i < scan; i += 256) {
+      const bool ok = valid(i);
+      if (ok && i < r0) ++before;
+      if (ok && p.d_loss) gm = max_or_nan(gm, fabsf(p.d_loss[i]));
     }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     before += __shfl_xor_sync(0xffffffffu, before, o);
-    const float y = __shfl_xor_sync(0xffffffffu, gm, o);
-    gm = (y > gm || y != y) ? y : gm;
+    gm = max_or_nan(gm, __shfl_xor_sync(0xffffffffu, gm, o));
   }
   if (lane == 0) { s_count[warp] = before; s_max[warp] = gm; }
   __syncthreads();
@@ -1069,8 +1095,7 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
   gm = 0.f;
   for (int w = 0; w < 8; ++w) {
     before += s_count[w];
-    const float y = s_max[w];
-    gm = (y > gm || y != y) ? y : gm;
+    gm = max_or_nan(gm, s_max[w]);
   }
   if (threadIdx.x == 0 && blockIdx.x == 0) {
     if (p.clear_err) *p.err = 0;
@@ -1265,6 +1290,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const float* part, int s
 // ---------------------------------------------------------------------------
 // Host side.
 
+constexpr int COUNTED_FROM = 16384;                // rows from which the gradient counts them first
 constexpr int LOSS_ROWS = 8192;                    // rows per forward pass: bounds the (max, sum) workspace
 constexpr long long P_BYTES = 256ll << 20;         // P of one vocabulary piece
 
@@ -1287,7 +1313,7 @@ int few_cols(int n) { return n <= 16 ? 16 : FEW_ROWS; }
 // Workspace of one call, laid out in order.
 struct Layout {
   int planes, rows, g_rows, two_terms, pieces, vc, splits, k_split, n_parts;
-  size_t block_err, n_valid, g_max, rows_b, perm, target, g, lse, tlogit, part, head, p, dh, total;
+  size_t block_err, counts, n_valid, g_max, rows_b, perm, target, g, lse, tlogit, part, head, p, dh, total;
   Layout(int n, int v, int d, bool f32, bool grad) {
     planes = f32 ? 3 : 1;
     // P beside bf16 operands is one bf16 term; for few rows two (few roundings do
@@ -1320,6 +1346,7 @@ struct Layout {
     size_t o = 256;   // the error word
     auto take = [&](size_t bytes) { const size_t at = o; o += up256(bytes); return at; };
     block_err = take(148 * 4);
+    counts = take(grad && n > COUNTED_FROM ? (size_t)div_up(n, COUNT_ROWS) * 8 : 0);
     n_valid = take(4);
     g_max = take(4);
     rows_b = take((size_t)planes * (grad ? g_rows : rows) * d * 2);
@@ -1434,8 +1461,7 @@ cudaError_t launch_products(const LossMaps& maps, const LossParams& p, long long
 }
 
 cudaError_t launch_order_rows(RowParams rp, bool f32, cudaStream_t st) {
-  // blocks scan the targets before them: few rows each while that is cheap
-  rp.rows_per_block = rp.n <= 2048 ? 4 : (rp.n <= 16384 ? 16 : 64);
+  rp.rows_per_block = rp.n <= 2048 ? 4 : (rp.n <= COUNTED_FROM ? 16 : 64);   // 64 divides COUNT_ROWS
   const int grid = div_up(rp.n > rp.twice ? rp.n : rp.twice, rp.rows_per_block);
   if (f32) order_rows_kernel<float><<<grid, 256, 0, st>>>(rp);
   else order_rows_kernel<bf16><<<grid, 256, 0, st>>>(rp);
@@ -1577,6 +1603,11 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
   rp.twice = L.two_terms;
   rp.d_loss = d_loss; rp.lse_in = lse; rp.g = (float*)(ws + L.g); rp.lse = (float*)(ws + L.lse);
   rp.g_max = (float*)(ws + L.g_max);
+  if (e == cudaSuccess && n > COUNTED_FROM) {
+    rp.counts = (const int2*)(ws + L.counts);
+    count_rows_kernel<<<div_up(n, COUNT_ROWS), COUNT_ROWS, 0, st>>>(rp, (int2*)(ws + L.counts));
+    e = cudaGetLastError();
+  }
   if (e == cudaSuccess) e = launch_order_rows(rp, f32, st);
   LossMaps mp{}, mg{};   // PROB, GRAD
   if (e == cudaSuccess) e = load_map(&mp.a, ws + L.rows_b, d, d, L.g_rows, L.planes);
@@ -1602,7 +1633,7 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     else if (few) e = load_map(&mg.a, ws + L.p, n, few_cols(n), p.vc, L.planes);
     else e = load_map(&mg.a, ws + L.p, p.vc, pitch, n, L.planes);
     if (e == cudaSuccess && !few) e = make_map(&mp.out0, ws + L.p, false, p.vc, pitch, n, L.planes, 64, 32);
-    p.chunk = f32 ? F32_CHUNK : 1 << 30;
+    p.chunk = f32 ? F32_CHUNK : WHOLE_CHUNK;
     const int nt = div_up(p.vc, TILE);
     p.p_out = (bf16*)(ws + L.p);
     p.p_trans = few;

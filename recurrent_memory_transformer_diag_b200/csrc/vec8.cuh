@@ -66,6 +66,8 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline armt_status check_sizes(armt_dtype dtype, int n, int v, int d) {
   if (n < 1 || v < 1 || d < 1) return ARMT_ERR_INVALID_ARG;
   if (dtype != ARMT_BF16 && dtype != ARMT_FP32) return ARMT_ERR_INVALID_ARG;
+  // 32-bit row and entry numbers with room for a grid's step
+  if (n > (1 << 30) || v > (1 << 30) || d > (1 << 20)) return ARMT_ERR_UNSUPPORTED;
   return d % 8 ? ARMT_ERR_UNSUPPORTED : ARMT_OK;
 }
 

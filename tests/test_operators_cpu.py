@@ -34,6 +34,9 @@ def test_workspace_sizes(libarmt):
     ("armt_embed_grad_workspace", (1, 0, 8, 64), INVALID), ("armt_embed_grad_workspace", (1, 8, 0, 64), INVALID),
     ("armt_embed_grad_workspace", (2, 8, 8, 64), INVALID), ("armt_embed_grad_workspace", (1, 8, 8, 60), UNSUPPORTED),
     ("armt_rms_norm_grad_workspace", (1, 8, 16392), UNSUPPORTED), ("armt_rms_norm_grad_workspace", (3, 8, 64), INVALID),
+    ("armt_embed_grad_workspace", (1, (1 << 30) + 1, 8, 64), UNSUPPORTED),
+    ("armt_token_loss_workspace", (1, 8, (1 << 30) + 1, 64, 0), UNSUPPORTED),
+    ("armt_token_loss_workspace", (1, 8, 8, (1 << 20) + 8, 0), UNSUPPORTED),
     ("armt_rms_norm_grad_workspace", (0, 8, -8), INVALID), ("armt_token_loss_workspace", (1, -1, 8, 64, 0), INVALID),
     ("armt_token_loss_workspace", (1, 8, 8, 64, 2), INVALID), ("armt_token_loss_workspace", (0, 8, 8, 4, 1), UNSUPPORTED),
 ])

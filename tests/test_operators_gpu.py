@@ -314,6 +314,8 @@ def test_token_loss_and_gradient(n, v, d, dtype):
     (8200, 300, 64, BF),       # two passes over the rows
     (8192, 17000, 64, BF),     # two pieces of the vocabulary in the gradient, the second ragged
     (4100, 11003, 64, FP),     # the same for fp32 operands
+    (20011, 515, 32, BF),      # rows counted before they are ordered
+    (17000, 257, 24, FP),
 ])
 def test_token_loss_in_pieces(n, v, d, dtype):
     hidden, head, t, w = loss_inputs(n, n, v, d, dtype)
@@ -372,6 +374,18 @@ def test_token_loss_not_a_number():
     assert torch.isnan(loss[7]) and torch.equal(loss[rest], clean[0][rest])
     assert torch.isnan(dh[7]).all() and torch.equal(dh[rest], clean[2][rest])
     assert torch.isnan(dw).any()
+
+
+def test_token_loss_range_of_fp32():
+    """Numbers above bf16's largest and tiny ones (all three terms still normal) keep their value."""
+    n, v, d = 33, 300, 64
+    hidden, head, t, w = loss_inputs(5, n, v, d, FP, ignored=0.0)
+    hidden[0], head[:, 0] = 0.0, 0.0
+    hidden[0, 0] = 3.4e38
+    head[7, 0] = 1e-30
+    head[8, 0] = -2e-30
+    got = run_loss(hidden, head, t, w)
+    check_loss(hidden, head, t, w, 1.0, got)
 
 
 def test_token_loss_weight_range():
