@@ -12,6 +12,7 @@ unless the caller passes one (a uint8 tensor of ``workspace_bytes`` bytes).
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -34,9 +35,9 @@ def _tensor(where: str, name: str, t, dtype, shape, device):
     """One dense tensor of this type and shape on this device."""
     if not isinstance(t, torch.Tensor):
         _bad(where, f"{name} must be a tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         _bad(where, f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != device:
+    if t.get_device() != device.index:
         _bad(where, f"{name} is on {t.device}, not on {device}")
     if t.shape != shape:
         _bad(where, f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
@@ -46,28 +47,31 @@ def _tensor(where: str, name: str, t, dtype, shape, device):
 
 def _matrix(where: str, name: str, t):
     """(library type, rows, columns, device) of the tensor the others go by."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in _TYPES:
+    kind = _TYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if kind is None or t.dim() != 2:
         _bad(where, f"{name} must be a 2-d tensor, bfloat16 or float32")
     if not t.is_cuda:
         _bad(where, f"{name} must be on a CUDA device")
     if not t.is_contiguous():
         _bad(where, f"{name} must be contiguous")
-    return _TYPES[t.dtype], t.shape[0], t.shape[1], t.device
+    n, d = t.shape
+    return kind, n, d, t.device
 
 
 def _ids(where: str, name: str, t, n: Optional[int], device) -> int:
-    if not isinstance(t, torch.Tensor) or t.dtype not in _ID_BYTES:
+    size = _ID_BYTES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if size is None:
         _bad(where, f"{name} must be an int32 or int64 tensor")
-    if t.device != device:
+    if t.get_device() != device.index:
         _bad(where, f"{name} is on {t.device}, not on {device}")
     if not t.is_contiguous() or t.dim() != 1 or (n is not None and t.shape[0] != n):
         _bad(where, f"{name} must be contiguous, one id per row")
-    return _ID_BYTES[t.dtype]
+    return size
 
 
 def _apart(where: str, outputs, others):
     """No output shares memory with an input or another output."""
-    spans = [(name, t.data_ptr(), t.nbytes) for name, t in others if t is not None]
+    spans = [(name, t.data_ptr(), t.nbytes) for name, t in others if isinstance(t, torch.Tensor)]
     for name, t in outputs:
         a, size = t.data_ptr(), t.nbytes
         for other, b, n in spans:
@@ -93,7 +97,7 @@ def on_stream(stream, device):
     """Make `device` and `stream` (a PyTorch stream, a raw handle, or None for the
     device's current one) current, so that what is allocated inside belongs to it."""
     if stream is None:
-        return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        return _HERE if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     if stream.device != device:
@@ -105,21 +109,28 @@ def _handle(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+@functools.lru_cache(maxsize=256)
+def _need(size_fn: str, args) -> int:
+    """Bytes of workspace, a function of the sizes alone."""
+    need = ctypes.c_size_t()
+    _check(getattr(lib(), size_fn)(*args, ctypes.byref(need)), size_fn)
+    return need.value
+
+
 def _space(where: str, size_fn: str, args, workspace, device):
     """(address, bytes, tensor to keep until the launches are made)."""
-    need = ctypes.c_size_t()
-    _check(getattr(lib(), size_fn)(*args, ctypes.byref(need)), where)
+    need = _need(size_fn, args)
     if workspace is None:
-        if need.value == 0:
+        if need == 0:
             return None, 0, None
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
     else:
         if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             _bad(where, "workspace must be a contiguous uint8 tensor")
-        if workspace.device != device:
+        if workspace.get_device() != device.index:
             _bad(where, f"workspace is on {workspace.device}, not on {device}")
-        if workspace.numel() < need.value:
-            _bad(where, f"workspace holds {workspace.numel()} bytes, {need.value} are needed")
+        if workspace.numel() < need:
+            _bad(where, f"workspace holds {workspace.numel()} bytes, {need} are needed")
     return workspace.data_ptr(), workspace.numel(), workspace
 
 
@@ -129,16 +140,13 @@ def workspace_bytes(op: str, dtype: torch.dtype, n: int, d: int, vocab: int = 1)
     t = _TYPES.get(dtype)
     if t is None:
         _bad("workspace_bytes", f"no operator takes {dtype}")
-    need = ctypes.c_size_t()
     calls = {"embed_grad": ("armt_embed_grad_workspace", (t, n, vocab, d)),
              "rms_norm_grad": ("armt_rms_norm_grad_workspace", (t, n, d)),
              "token_loss": ("armt_token_loss_workspace", (t, n, vocab, d, 0)),
              "token_loss_grad": ("armt_token_loss_workspace", (t, n, vocab, d, 1))}
     if op not in calls:
         _bad("workspace_bytes", f"unknown operator {op!r}")
-    name, args = calls[op]
-    _check(getattr(lib(), name)(*args, ctypes.byref(need)), name)
-    return need.value
+    return _need(*calls[op])
 
 
 def workspace_status(workspace, stream=None):

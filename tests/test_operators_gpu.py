@@ -579,3 +579,73 @@ def test_score_runs_ids_to_losses(name):
             parts.append(p)
         torch.cuda.synchronize()
         assert torch.equal(torch.cat(parts), loss)
+
+
+# ------------------------------------------------------------------ refusals
+def _refusals():
+    z = lambda *s, dt=BF: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+    n, v, d = 6, 20, 64
+    base = {"x": z(n, d), "y": z(n, d), "dy": z(n, d), "dx": z(n, d), "w": z(v, d), "dw": z(v, d), "gain": z(d),
+            "dg": z(d), "f": z(n, dt=FP), "f2": z(n, dt=FP), "f3": z(n, dt=FP),
+            "i": torch.zeros(n, dtype=torch.int64, device="cuda")}
+    calls = {
+        "embed": lambda o, b: o.embed(b["i"], b["w"], b["y"]),
+        "embed_grad": lambda o, b: o.embed_grad(b["i"], b["dy"], b["dw"]),
+        "rms_norm": lambda o, b: o.rms_norm(b["x"], b["gain"], b["y"], b["f"]),
+        "rms_norm_grad": lambda o, b: o.rms_norm_grad(b["x"], b["gain"], b["f"], b["dy"], b["dx"], b["dg"]),
+        "token_loss": lambda o, b: o.token_loss(b["x"], b["w"], b["i"], b["f"], b["f2"]),
+        "token_loss_grad": lambda o, b: o.token_loss_grad(b["x"], b["w"], b["i"], b["f"], b["f2"], b["dx"], b["dw"]),
+    }
+    shift = lambda *s: torch.zeros(math.prod(s) + 1, dtype=BF, device="cuda")[1:].view(*s)  # noqa: E731
+    return base, calls, [
+        ("embed", "w", z(v, d, dt=torch.float16)), ("embed", "w", z(v, d).t()), ("embed", "w", shift(v, d)),
+        ("embed", "i", z(n)), ("embed", "i", z(2 * n).long()[::2]), ("embed", "y", z(n, d, dt=FP)),
+        ("embed", "y", z(n + 1, d)), ("embed", "y", base["w"][:n]), ("embed", "w", z(v, 60)), ("embed", "y", z(n, d).cpu()),
+        ("embed_grad", "dw", z(v, d + 8)), ("embed_grad", "dw", z(v * d)), ("embed_grad", "i", z(n + 1).long()),
+        ("embed_grad", "dy", z(n, 2 * d)[:, :d]), ("embed_grad", "dw", base["dy"]), ("embed_grad", "dw", None),
+        ("rms_norm", "gain", z(d, dt=FP)), ("rms_norm", "f", z(n)), ("rms_norm", "y", base["x"].view(-1)[d:].new_zeros(n, d + 8)),
+        ("rms_norm", "x", z(n, d, 1)), ("rms_norm", "gain", z(d + 8)), ("rms_norm", "y", None),
+        ("rms_norm_grad", "dx", base["gain"].expand(n, d)), ("rms_norm_grad", "dg", base["x"][0]),
+        ("rms_norm_grad", "f", z(n + 1, dt=FP)), ("rms_norm_grad", "dy", z(n, d, dt=FP)),
+        ("token_loss", "w", z(v, d, dt=FP)), ("token_loss", "i", z(n, 1).long()), ("token_loss", "f", z(n)),
+        ("token_loss", "f2", base["f"]), ("token_loss", "x", shift(n, d)), ("token_loss", "w", z(v, d + 8)),
+        ("token_loss_grad", "dx", base["x"]), ("token_loss_grad", "dw", base["w"]), ("token_loss_grad", "f2", z(n)),
+        ("token_loss_grad", "dw", z(v, d, dt=FP)), ("token_loss_grad", "dx", z(n, d).t()),
+        ("token_loss_grad", "i", z(n).to(torch.int16)),
+    ]
+
+
+@pytest.mark.parametrize("k", range(38))
+def test_wrappers_refuse(k):
+    """One wrong tensor at a time: an error, and nothing is written."""
+    from recurrent_memory_transformer_diag_b200 import ArmtError, operators as ops
+    base, calls, wrong = _refusals()
+    assert len(wrong) == 38
+    op, name, t = wrong[k]
+    before = {q: u.clone() for q, u in base.items()}
+    with pytest.raises(ArmtError) as e:
+        calls[op](ops, {**base, name: t})
+    assert e.value.status in (1, 7)
+    torch.cuda.synchronize()
+    assert all(torch.equal(before[q], base[q]) for q in base)
+
+
+def test_wrappers_refuse_workspaces():
+    from recurrent_memory_transformer_diag_b200 import ArmtError, embed_grad, token_loss, workspace_bytes
+    n, v, d = 200, 300, 64
+    hidden, head, t, w = loss_inputs(1, n, v, d, BF)
+    loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    size = workspace_bytes("token_loss", BF, n, d, v)
+    for ws in (torch.empty(size - 1, dtype=torch.uint8, device="cuda"), torch.empty(size, dtype=torch.uint8),
+               torch.empty(size // 4 + 1, device="cuda"), torch.empty(size + 8, dtype=torch.uint8, device="cuda")[8:],
+               torch.empty(2 * size, dtype=torch.uint8, device="cuda")[::2], 5):
+        with pytest.raises(ArmtError):
+            token_loss(hidden, head, t, loss, lse, workspace=ws)
+    out = torch.empty(v, d, dtype=BF, device="cuda")
+    size = workspace_bytes("embed_grad", BF, n, d, v)
+    assert size > 0
+    with pytest.raises(ArmtError):
+        embed_grad(t, hidden, out, workspace=torch.empty(size - 1, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ArmtError):   # results inside the workspace
+        ws = torch.empty(size + v * d * 2, dtype=torch.uint8, device="cuda")
+        embed_grad(t, hidden, ws[:v * d * 2].view(BF).view(v, d), workspace=ws)
