@@ -81,6 +81,7 @@ struct LossParams {
   int two_terms;              // GRAD, few bf16 rows: the second terms of P stand as further rows, this far behind
   int planes;                 // 1: bf16 operands; 3: fp32 operands as three bf16 terms
   int v0, vc;                 // vocabulary piece
+  int panels;                 // P is kept in panels of 64 columns: [term][panel][row][64], 4 to 8 KB a copy
   int chunk;                  // k-blocks per accumulator
   float scale;
   const int* n_valid;         // rows with a target (device)
@@ -95,6 +96,7 @@ struct LossParams {
   const void* ids; int id_bytes; unsigned* block_err;
   // GRAD
   int want_dw, want_dh, splits, k_split, dh_add, dw_bf16;
+  int dw_splits, dw_k;        // dW's contraction in splits of dw_k rows, as partial sums where there are several
   const float* g_max;
   unsigned* err;
 };
@@ -134,10 +136,10 @@ struct Jobs {
     nt = (p.vc + TILE - 1) / TILE;
     dt = (p.d + TILE - 1) / TILE;
     if (ROLE == GRAD) {
-      n_dw = p.want_dw ? nt * dt : 0;
+      n_dw = p.want_dw ? nt * dt * p.dw_splits : 0;
       n_dh = p.want_dh ? mt * dt * p.splits : 0;
       total = n_dw + n_dh;
-      dw_first = nv >= p.k_split;
+      dw_first = min(nv, p.dw_k) >= p.k_split;
     } else {
       n_dw = n_dh = 0;
       dw_first = false;
@@ -162,12 +164,14 @@ struct Jobs {
       j.ka = j.kb = 0;
       j.kblocks = (p.d + BK - 1) / BK;
     } else if (dw_first ? t < n_dw : t >= n_dh) {
-      const int r = dw_first ? t : t - n_dh;
+      int r = dw_first ? t : t - n_dh;
       j.dw = true;
-      j.m0 = (r / dt) * TILE;
       j.n0 = (r % dt) * TILE;
-      j.ka = j.kb = 0;
-      j.kblocks = (nv + BK - 1) / BK;
+      r /= dt;
+      j.m0 = (r % nt) * TILE;
+      j.split = r / nt;
+      j.ka = j.kb = j.split * p.dw_k;
+      j.kblocks = (max(min(nv - j.ka, p.dw_k), 0) + BK - 1) / BK;
     } else {
       int r = dw_first ? t - n_dw : t;
       j.n0 = (r % dt) * TILE;
@@ -344,7 +348,7 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
     for (int h = 0; h < 2; ++h) {
       if (wrow0 >= p.n_rows || pc + 64 * h >= p.vc) continue;   // nothing of this box is in P
       for (int t = 0; t < p.planes; ++t) {
-        emit_bf16x64(&maps.out0, slot(), lane, sums + 32 * h, pc + 64 * h, wrow0, t);
+        emit_bf16x64(&maps.out0, slot(), lane, sums + 32 * h, 0, wrow0, t * p.panels + pc / 64 + h);
         if (t + 1 < p.planes) {   // what the term just written leaves of the value
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -357,6 +361,13 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
   } else {
     if (j.dw) {
       if (wrow0 >= p.vc) return;
+      if (p.dw_splits > 1) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          if (col0 + 32 * h < p.d)
+            emit_f32x32(&maps.out0, slot(), lane, sums + 16 * h, col0 + 32 * h, wrow0, j.split, false);
+        return;
+      }
       const float f = *p.g_max * p.scale;
       const float2 f2 = make_float2(f, f);
 #pragma unroll
@@ -476,7 +487,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           const int ka = j.ka + kb * BK, kbb = j.kb + kb * BK;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            tma_load_3d_pair(ma, fb, sa + h * BOX_BYTES, a_mn ? am + 64 * h : ka, a_mn ? ka : am + 64 * h, ta);
+            const int row = am + 64 * h;
+            if (ROLE == GRAD && !p.p_trans)
+              tma_load_3d_pair(ma, fb, sa + h * BOX_BYTES, 0, a_mn ? ka : row, ta * p.panels + (a_mn ? row : ka) / BK);
+            else
+              tma_load_3d_pair(ma, fb, sa + h * BOX_BYTES, a_mn ? row : ka, a_mn ? ka : row, ta);
             if (128 * h < j.n)
               tma_load_3d_pair(mb, fb, sa + (2 + h) * BOX_BYTES, b_mn ? bn + 64 * h : kbb, b_mn ? kbb : bn + 64 * h,
                                tb);
@@ -1039,13 +1054,13 @@ __device__ __forceinline__ float max_or_nan(float a, float b) { return (b > a ||
 
 // counts[k]: rows with a target among 1024 k .. 1024 k + 1023, and their largest
 // |weight|.  Without it every block of order_rows looks through all rows, which
-// is cheap up to some 10^4 of them only.
+// is cheap for few of them only.
 constexpr int COUNT_ROWS = 1024;
 __global__ void __launch_bounds__(COUNT_ROWS) count_rows_kernel(const RowParams p, int2* counts) {
   __shared__ float s_max[32];
   const int i = blockIdx.x * COUNT_ROWS + threadIdx.x;
   const bool ok = i < p.n && target_of(p.targets, p.target_bytes, i, p.vocab) >= 0;
-  float gm = ok ? fabsf(p.d_loss[i]) : 0.f;
+  float gm = ok && p.d_loss ? fabsf(p.d_loss[i]) : 0.f;
   const int count = __syncthreads_count(ok);
 #pragma unroll
   for (int o = 16; o; o >>= 1) gm = max_or_nan(gm, __shfl_xor_sync(0xffffffffu, gm, o));
@@ -1078,10 +1093,20 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
     for (int i = here * COUNT_ROWS + threadIdx.x; i < r0; i += 256) before += valid(i);
   } else {
     const int scan = p.d_loss ? p.n : min(r0, p.n);
-    for (int i = threadIdx.x; i < scan; i += 256) {
-      const bool ok = valid(i);
-      if (ok && i < r0) ++before;
-      if (ok && p.d_loss) gm = max_or_nan(gm, fabsf(p.d_loss[i]));
+    for (int i0 = threadIdx.x; i0 < scan; i0 += 4 * 256) {   // four rows in flight
+      bool ok[4];
+      float g[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * 256;
+        ok[u] = i < scan && valid(i);
+        g[u] = p.d_loss && i < scan ? fabsf(p.d_loss[i]) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        before += ok[u] && i0 + u * 256 < r0;
+        if (ok[u]) gm = max_or_nan(gm, g[u]);
+      }
     }
   }
 #pragma unroll
@@ -1241,48 +1266,66 @@ __global__ void __launch_bounds__(1024) join_lse_kernel(const JoinParams p) {
   }
 }
 
-// dH rows back in their order: the splits' partial sums (of `rows` rows; with
-// two terms of P those of both) added in order, times
-// the weights' common factor.  After a wait that ran out, NaN there and in the
-// head's gradient.  Either may be null.
-template <typename T>
-__global__ void __launch_bounds__(256) join_rows_kernel(const float* part, int splits, int rows, int two_terms, int n,
-                                                        int d, const int* perm,
-                                                        const int* n_valid, const float* g_max, float scale,
-                                                        const unsigned* err, T* out, T* head, long long head_n) {
-  const int nv = *n_valid;
-  const bool bad = *err != 0;
-  if (bad && head) {
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < head_n; i += (long long)gridDim.x * 256)
-      head[i] = (T)NAN;
+// Partial sums of a gradient, [splits][rows][d], added in order, times the
+// weights' common factor.  Rows of dH go to their places (perm), those without
+// a target become zero, and with two terms of P a row is the sum of two.  G
+// groups of splits side by side, 1024 / G columns a block and step.  After a
+// wait that ran out: NaN here and in all of `head`, where that is given.
+struct JoinRows {
+  const float* part; int splits, rows, two_terms, n, d;
+  const int* perm; const int* n_valid;
+  const float* g_max; float scale;
+  const unsigned* err;
+  void* out; void* head; long long head_n;
+};
+
+template <typename T, int G>
+__global__ void __launch_bounds__(256) join_rows_kernel(const JoinRows p) {
+  constexpr int X = 256 / G;
+  __shared__ float4 s[G][X];
+  const int x = threadIdx.x % X, y = threadIdx.x / X;
+  const bool bad = *p.err != 0;
+  if (bad && p.head) {
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < p.head_n; i += (long long)gridDim.x * 256)
+      reinterpret_cast<T*>(p.head)[i] = (T)NAN;
   }
-  if (!out) return;
-  const float f = *g_max * scale;
-  const int vecs = d / 4;
-  const long long total = (long long)n * vecs, plane = (long long)rows * d;
-  for (long long k = (long long)blockIdx.x * 256 + threadIdx.x; k < total; k += (long long)gridDim.x * 256) {
+  if (!p.out) return;
+  const int nv = p.perm ? *p.n_valid : p.n;
+  const float f = *p.g_max * p.scale;
+  const int vecs = p.d / 4, per = (p.splits + G - 1) / G;
+  const long long total = (long long)p.n * vecs, plane = (long long)p.rows * p.d;
+  for (long long k0 = (long long)blockIdx.x * X; k0 < total; k0 += (long long)gridDim.x * X) {
+    const long long k = k0 + x;
     const int r = (int)(k / vecs), c = (int)(k - (long long)r * vecs) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (bad) v = make_float4(NAN, NAN, NAN, NAN);
-    if (r < nv && !bad) {
-#pragma unroll 8
-      for (int s = 0; s < splits; ++s) {
-        const float4 a = *reinterpret_cast<const float4*>(part + s * plane + (long long)r * d + c);
-        v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
-        if (two_terms) {
-          const float4 b = *reinterpret_cast<const float4*>(part + s * plane + (long long)(r + two_terms) * d + c);
-          v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
-        }
+    auto add = [&](float4 a) { v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w; };
+    if (k < total && r < nv) {
+#pragma unroll 4
+      for (int i = y * per; i < min(p.splits, (y + 1) * per); ++i) {
+        const float* at = p.part + i * plane + (long long)r * p.d + c;
+        add(*reinterpret_cast<const float4*>(at));
+        if (p.two_terms) add(*reinterpret_cast<const float4*>(at + (long long)p.two_terms * p.d));
       }
-      v.x *= f; v.y *= f; v.z *= f; v.w *= f;
     }
-    T* dst = out + (long long)perm[r] * d + c;
-    if constexpr (sizeof(T) == 2) {
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    } else {
-      *reinterpret_cast<float4*>(dst) = v;
+    if constexpr (G > 1) {
+      __syncthreads();
+      s[y][x] = v;
+      __syncthreads();
+      if (y == 0)
+        for (int g = 1; g < G; ++g) add(s[g][x]);
+    }
+    if (y == 0 && k < total) {
+      v.x *= f; v.y *= f; v.z *= f; v.w *= f;
+      if (r >= nv) v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (bad) v = make_float4(NAN, NAN, NAN, NAN);
+      T* dst = reinterpret_cast<T*>(p.out) + (long long)(p.perm ? p.perm[r] : r) * p.d + c;
+      if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      } else {
+        *reinterpret_cast<float4*>(dst) = v;
+      }
     }
   }
 }
@@ -1290,7 +1333,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const float* part, int s
 // ---------------------------------------------------------------------------
 // Host side.
 
-constexpr int COUNTED_FROM = 16384;                // rows from which the gradient counts them first
+constexpr int COUNTED_FROM = 2048;                 // rows from which they are counted first (8192 rows: 13 + 3 us, 37 without)
 constexpr int LOSS_ROWS = 8192;                    // rows per forward pass: bounds the (max, sum) workspace
 constexpr long long P_BYTES = 256ll << 20;         // P of one vocabulary piece
 
@@ -1312,8 +1355,8 @@ int few_cols(int n) { return n <= 16 ? 16 : FEW_ROWS; }
 
 // Workspace of one call, laid out in order.
 struct Layout {
-  int planes, rows, g_rows, two_terms, pieces, vc, splits, k_split, n_parts;
-  size_t block_err, counts, n_valid, g_max, rows_b, perm, target, g, lse, tlogit, part, head, p, dh, total;
+  int planes, rows, g_rows, two_terms, pieces, vc, splits, k_split, dw_splits, dw_k, n_parts;
+  size_t block_err, counts, n_valid, g_max, rows_b, perm, target, g, lse, tlogit, part, head, p, dh, dw, total;
   Layout(int n, int v, int d, bool f32, bool grad) {
     planes = f32 ? 3 : 1;
     // P beside bf16 operands is one bf16 term; for few rows two (few roundings do
@@ -1324,7 +1367,7 @@ struct Layout {
     const bool simt = f32_few(f32, n, d, grad);
     rows = grad ? n : (n < LOSS_ROWS ? n : LOSS_ROWS);
     n_parts = simt ? 148 * (F32_FEW_THREADS / 32) : (n <= FEW_ROWS ? 4 * few_blocks(v) : 2 * div_up(v, TILE));
-    vc = v; pieces = 1; splits = k_split = 0;
+    vc = v; pieces = 1; splits = k_split = dw_k = 0; dw_splits = 1;
     if (grad) {
       long long w = P_BYTES / ((long long)g_rows * 2 * planes) / TILE * TILE;
       if (w < TILE) w = TILE;
@@ -1339,6 +1382,13 @@ struct Layout {
       const long long blocks = dt * (mt * div_up(vc, BK) + nt * div_up(g_rows, BK));
       const long long want = blocks / (4 * 74);
       const int ks = BK * (int)(want < 4 ? 4 : (want > 128 ? 128 : want));
+      // dW likewise where its tiles alone would not fill the device
+      if (nt * dt * 2 <= 74 && g_rows > 512) {
+        const int most = div_up(g_rows, 256), fill = div_up(74, (int)(nt * dt));
+        dw_splits = most < fill ? most : fill;
+      }
+      dw_k = round_up(div_up(g_rows, dw_splits), BK);
+      dw_splits = div_up(g_rows, dw_k);
       splits = div_up(vc, ks);
       k_split = round_up(div_up(vc, splits), BK);
       splits = div_up(vc, k_split);
@@ -1346,7 +1396,7 @@ struct Layout {
     size_t o = 256;   // the error word
     auto take = [&](size_t bytes) { const size_t at = o; o += up256(bytes); return at; };
     block_err = take(148 * 4);
-    counts = take(grad && n > COUNTED_FROM ? (size_t)div_up(n, COUNT_ROWS) * 8 : 0);
+    counts = take(rows > COUNTED_FROM ? (size_t)div_up(rows, COUNT_ROWS) * 8 : 0);
     n_valid = take(4);
     g_max = take(4);
     rows_b = take((size_t)planes * (grad ? g_rows : rows) * d * 2);
@@ -1359,6 +1409,7 @@ struct Layout {
     head = take(f32 && !simt ? (size_t)3 * v * d * 2 : 0);
     p = take(grad ? (size_t)planes * (two_terms ? g_rows : (n <= FEW_ROWS ? few_cols(n) : n)) * round_up(vc, 64) * 2 : 0);
     dh = take(grad ? (size_t)splits * g_rows * d * 4 : 0);
+    dw = take(dw_splits > 1 ? (size_t)dw_splits * vc * d * 4 : 0);
     total = o;
   }
 };
@@ -1460,8 +1511,25 @@ cudaError_t launch_products(const LossMaps& maps, const LossParams& p, long long
   return cudaGetLastError();
 }
 
-cudaError_t launch_order_rows(RowParams rp, bool f32, cudaStream_t st) {
-  rp.rows_per_block = rp.n <= 2048 ? 4 : (rp.n <= COUNTED_FROM ? 16 : 64);   // 64 divides COUNT_ROWS
+cudaError_t launch_join_rows(const JoinRows& jr, bool f32, cudaStream_t st) {
+  const bool groups = jr.splits >= 8;
+  const long long blocks = ((long long)jr.n * (jr.d / 4) + (groups ? 31 : 255)) / (groups ? 32 : 256);
+  const int grid = (int)(blocks < 148 * 16 ? blocks : 148 * 16);
+  if (f32 && groups) join_rows_kernel<float, 8><<<grid, 256, 0, st>>>(jr);
+  else if (f32) join_rows_kernel<float, 1><<<grid, 256, 0, st>>>(jr);
+  else if (groups) join_rows_kernel<bf16, 8><<<grid, 256, 0, st>>>(jr);
+  else join_rows_kernel<bf16, 1><<<grid, 256, 0, st>>>(jr);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_order_rows(RowParams rp, bool f32, int2* counts, cudaStream_t st) {
+  rp.rows_per_block = rp.n <= 2048 ? 4 : (rp.n <= 65536 ? 16 : 64);   // both divide COUNT_ROWS
+  if (rp.n > COUNTED_FROM) {
+    rp.counts = counts;
+    count_rows_kernel<<<div_up(rp.n, COUNT_ROWS), COUNT_ROWS, 0, st>>>(rp, counts);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   const int grid = div_up(rp.n > rp.twice ? rp.n : rp.twice, rp.rows_per_block);
   if (f32) order_rows_kernel<float><<<grid, 256, 0, st>>>(rp);
   else order_rows_kernel<bf16><<<grid, 256, 0, st>>>(rp);
@@ -1562,7 +1630,7 @@ extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d
     rp.rows = (bf16*)(ws + L.rows_b); rp.perm = (int*)(ws + L.perm); rp.target = (int*)(ws + L.target);
     rp.n_valid = (int*)(ws + L.n_valid); rp.err = (unsigned*)ws;
     rp.loss_out = loss + r0; rp.lse_out = lse + r0;
-    e = launch_order_rows(rp, f32, st);
+    e = launch_order_rows(rp, f32, (int2*)(ws + L.counts), st);
     if (e == cudaSuccess)
       e = few ? few_map(&maps.a, ws + L.rows_b, nr, d, L.planes) : load_map(&maps.a, ws + L.rows_b, d, d, nr, L.planes);
     if (e != cudaSuccess) break;
@@ -1603,36 +1671,35 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
   rp.twice = L.two_terms;
   rp.d_loss = d_loss; rp.lse_in = lse; rp.g = (float*)(ws + L.g); rp.lse = (float*)(ws + L.lse);
   rp.g_max = (float*)(ws + L.g_max);
-  if (e == cudaSuccess && n > COUNTED_FROM) {
-    rp.counts = (const int2*)(ws + L.counts);
-    count_rows_kernel<<<div_up(n, COUNT_ROWS), COUNT_ROWS, 0, st>>>(rp, (int2*)(ws + L.counts));
-    e = cudaGetLastError();
-  }
-  if (e == cudaSuccess) e = launch_order_rows(rp, f32, st);
+  if (e == cudaSuccess) e = launch_order_rows(rp, f32, (int2*)(ws + L.counts), st);
   LossMaps mp{}, mg{};   // PROB, GRAD
   if (e == cudaSuccess) e = load_map(&mp.a, ws + L.rows_b, d, d, L.g_rows, L.planes);
   if (e == cudaSuccess) e = load_map(&mp.b, w, d, d, vocab, L.planes);
   mg.b = mp.b;
   mg.c = mp.a;
-  if (e == cudaSuccess && d_head) e = make_map(&mg.out0, d_head, f32, d, d, vocab, 1, f32 ? 32 : 64, 32);
+  if (e == cudaSuccess && d_head)
+    e = L.dw_splits > 1 ? make_map(&mg.out0, ws + L.dw, true, d, d, L.vc, L.dw_splits, 32, 32)
+                        : make_map(&mg.out0, d_head, f32, d, d, vocab, 1, f32 ? 32 : 64, 32);
   if (e == cudaSuccess && d_hidden) e = make_map(&mg.out1, ws + L.dh, true, d, d, L.g_rows, L.splits, 32, 32);
   LossParams p{};
   p.n_rows = n; p.d = d; p.vocab = vocab; p.planes = L.planes; p.scale = scale;
   p.n_valid = rp.n_valid; p.target = rp.target; p.lse = rp.lse; p.g = rp.g; p.g_max = rp.g_max; p.err = rp.err;
   p.want_dw = d_head != nullptr; p.want_dh = d_hidden != nullptr; p.dw_bf16 = !f32; p.k_split = L.k_split;
+  p.dw_splits = L.dw_splits; p.dw_k = L.dw_k;
   const bool few = n <= FEW_ROWS;
   if (e == cudaSuccess && few) e = few_map(&mp.a, ws + L.rows_b, n, d, L.planes);
   if (e == cudaSuccess && few) e = few_head_map(&mp.b, w, vocab, d, L.planes);
-  const int pitch = round_up(L.vc, 64), mt = div_up(L.g_rows, TILE), dt = div_up(d, TILE);
+  const int mt = div_up(L.g_rows, TILE), dt = div_up(d, TILE);
   for (int v0 = 0; v0 < vocab && e == cudaSuccess; v0 += L.vc) {
     p.v0 = v0;
     p.vc = vocab - v0 < L.vc ? vocab - v0 : L.vc;
+    p.panels = div_up(p.vc, BK);
     p.splits = div_up(p.vc, L.k_split);
     p.dh_add = v0 > 0;
     if (L.two_terms) e = load_map(&mg.a, ws + L.p, L.g_rows, L.g_rows, p.vc, 1);
     else if (few) e = load_map(&mg.a, ws + L.p, n, few_cols(n), p.vc, L.planes);
-    else e = load_map(&mg.a, ws + L.p, p.vc, pitch, n, L.planes);
-    if (e == cudaSuccess && !few) e = make_map(&mp.out0, ws + L.p, false, p.vc, pitch, n, L.planes, 64, 32);
+    else e = load_map(&mg.a, ws + L.p, 64, 64, n, p.panels * L.planes);
+    if (e == cudaSuccess && !few) e = make_map(&mp.out0, ws + L.p, false, 64, 64, n, p.panels * L.planes, 64, 32);
     p.chunk = f32 ? F32_CHUNK : WHOLE_CHUNK;
     const int nt = div_up(p.vc, TILE);
     p.p_out = (bf16*)(ws + L.p);
@@ -1643,21 +1710,22 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     LossParams pg = p;
     pg.n_rows = L.g_rows;
     pg.two_terms = L.two_terms;
-    const long long jobs = (p.want_dw ? (long long)nt * dt : 0) + (p.want_dh ? (long long)mt * dt * p.splits : 0);
+    const long long jobs = (p.want_dw ? (long long)nt * dt * L.dw_splits : 0) + (p.want_dh ? (long long)mt * dt * p.splits : 0);
     if (e == cudaSuccess) e = launch_products<GRAD>(mg, pg, jobs, st);
+    if (e == cudaSuccess && d_head && L.dw_splits > 1) {
+      JoinRows jr{};
+      jr.part = (const float*)(ws + L.dw); jr.splits = L.dw_splits; jr.rows = L.vc; jr.n = p.vc; jr.d = d;
+      jr.g_max = rp.g_max; jr.scale = scale; jr.err = rp.err;
+      jr.out = (char*)d_head + (size_t)v0 * d * (f32 ? 4 : 2);
+      e = launch_join_rows(jr, f32, st);
+    }
   }
   if (e == cudaSuccess) {
-    const long long blocks = ((long long)n * (d / 4) + 255) / 256;
-    const int grid = d_hidden ? (int)(blocks < 148 * 16 ? blocks : 148 * 16) : 148;
-    const float* part = (const float*)(ws + L.dh);
-    const long long head_n = (long long)vocab * d;
-    if (f32)
-      join_rows_kernel<float><<<grid, 256, 0, st>>>(part, L.splits, L.g_rows, L.two_terms, n, d, rp.perm, rp.n_valid, rp.g_max, scale, rp.err,
-                                                    (float*)d_hidden, (float*)d_head, head_n);
-    else
-      join_rows_kernel<bf16><<<grid, 256, 0, st>>>(part, L.splits, L.g_rows, L.two_terms, n, d, rp.perm, rp.n_valid, rp.g_max, scale, rp.err,
-                                                   (bf16*)d_hidden, (bf16*)d_head, head_n);
-    e = cudaGetLastError();
+    JoinRows jr{};
+    jr.part = (const float*)(ws + L.dh); jr.splits = L.splits; jr.rows = L.g_rows; jr.two_terms = L.two_terms;
+    jr.n = n; jr.d = d; jr.perm = rp.perm; jr.n_valid = rp.n_valid; jr.g_max = rp.g_max; jr.scale = scale;
+    jr.err = rp.err; jr.out = d_hidden; jr.head = d_head; jr.head_n = (long long)vocab * d;
+    e = launch_join_rows(jr, f32, st);
   }
   return cuda_status(e);
 }

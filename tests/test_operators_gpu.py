@@ -294,7 +294,7 @@ LOSS = [
     # n, v, d
     (1, 1, 8), (1, 300, 64), (2, 255, 72), (3, 256, 64), (5, 257, 136), (127, 512, 256), (128, 1000, 64),
     (129, 1023, 328), (255, 1025, 64), (257, 777, 512), (300, 5003, 128), (64, 33000, 64), (1030, 259, 2048),
-    (4, 20000, 72), (16, 700, 200), (17, 515, 64), (65, 300, 64), (16, 300, 3208), (130, 2500, 136), (128, 700, 384),
+    (4, 20000, 72), (16, 700, 200), (17, 515, 64), (65, 300, 64), (16, 300, 3208), (2000, 300, 64), (1500, 1025, 136), (130, 2500, 136), (128, 700, 384),
 ]
 
 
