@@ -268,12 +268,31 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// What the epilogue needs of its row, loaded before it waits for the products.
+struct RowData {
+  int target;        // -1: none, or past the last row
+  float g, lse;      // PROB
+};
+
+template <int ROLE>
+__device__ __forceinline__ RowData load_row(const LossParams& p, int row, int nv) {
+  RowData r = {-1, 0.f, 0.f};
+  if (ROLE != GRAD && row < nv) {
+    r.target = p.target[row];
+    if (ROLE == PROB) {
+      r.g = p.g[row];
+      r.lse = p.lse[row];
+    }
+  }
+  return r;
+}
+
 // Epilogue of one tile: sums holds this thread's row (TMEM lane) of 128
 // columns, those of its half of the tile.
 template <int ROLE>
 __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps& maps, const Job& j, int nv,
-                                            float2 (&sums)[64], int row_in_tile, int half, int lane,
-                                            uint8_t* slots, int& turn) {
+                                            const RowData& rd, float2 (&sums)[64], int row_in_tile, int half,
+                                            int lane, uint8_t* slots, int& turn) {
   auto slot = [&] { return slots + (turn ^= 1) * SLOT_BYTES; };
   const int row = j.m0 + row_in_tile;
   const int wrow0 = row - lane;
@@ -307,7 +326,7 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
     s2[0] = __fadd2_rn(s2[0], s2[1]);
     if (row < nv) {
       p.part[(long long)(2 * j.ntile + half) * p.part_pitch + row] = make_float2(m, s2[0].x + s2[0].y);
-      const unsigned at = (unsigned)(p.target[row] - col0);
+      const unsigned at = (unsigned)(rd.target - col0);
       if (at < 128u) {
         float t = 0.f;
 #pragma unroll
@@ -319,9 +338,7 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
       }
     }
   } else if constexpr (ROLE == PROB) {
-    const bool in = row < nv;
-    const float g = in ? p.g[row] : 0.f;
-    const float lse = in ? p.lse[row] : 0.f;
+    const float g = rd.g, lse = rd.lse;
     const float2 scale2 = make_float2(p.scale, p.scale), neg = make_float2(-lse, -lse),
                  log2e = make_float2(LOG2E, LOG2E), g2 = make_float2(g, g);
 #pragma unroll
@@ -329,8 +346,8 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
       const float2 x = __fmul2_rn(__fadd2_rn(__fmul2_rn(sums[i], scale2), neg), log2e);
       sums[i] = __fmul2_rn(make_float2(ex2(x.x), ex2(x.y)), g2);
     }
-    if (in) {
-      const unsigned at = (unsigned)(p.target[row] - col0);
+    if (rd.target >= 0) {
+      const unsigned at = (unsigned)(rd.target - col0);
       if (at < 128u) {
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
@@ -575,9 +592,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     bool ok = !skip;
     for (int t = cid; t < jobs.total && ok; t += ncl) {
       const Job j = jobs.get(p, nv, t);
+      const RowData rd = load_row<ROLE>(p, j.m0 + row_in_tile, nv);
       float2 acc[64];   // this thread's row, 128 columns (pairs: two additions or products an instruction)
+      if (j.kblocks == 0) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
+        for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
+      }
       const int iters = products * j.kblocks;
       for (int it = 0; it < iters; it += p.chunk) {
         const bool got = mbar_wait_cluster(&tfull[buf], acc_phase, abort_flag);
@@ -589,19 +609,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         }
         tc_fence_after();
         const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * TILE + half * 128);
+        if (it == 0) {   // the first chunk straight into the sums
+          uint32_t v[2][64];
+          tmem_ld64_nowait(tbase, v[0]);
+          tmem_ld64_nowait(tbase + 64, v[1]);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tmem_ld32(tbase + (uint32_t)(c * 32), v);
+          for (int i = 0; i < 64; ++i)
+            acc[i] = make_float2(__uint_as_float(v[i / 32][2 * (i % 32)]), __uint_as_float(v[i / 32][2 * (i % 32) + 1]));
+        } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c * 16 + i] = __fadd2_rn(acc[c * 16 + i], make_float2(v[2 * i], v[2 * i + 1]));
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            tmem_ld32(tbase + (uint32_t)(c * 32), v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              acc[c * 16 + i] = __fadd2_rn(acc[c * 16 + i], make_float2(v[2 * i], v[2 * i + 1]));
+          }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
         if (++buf == 2) { buf = 0; acc_phase ^= 1; }
       }
-      if (ok) finish_tile<ROLE>(p, maps, j, nv, acc, row_in_tile, half, lane, slots, turn);
+      if (ok) finish_tile<ROLE>(p, maps, j, nv, rd, acc, row_in_tile, half, lane, slots, turn);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
