@@ -212,32 +212,22 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* s
                : "memory");
 }
 
-// The warp's other slot may be written (all but the last store have been read).
-__device__ __forceinline__ void slot_free(int lane) {
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-  __syncwarp();
-}
-
-// 16-byte piece q of this lane's row in the slot (128-byte swizzle).
+// 16-byte piece q of this lane's row in a slot (128-byte swizzle).
 __device__ __forceinline__ uint4* slot_piece(uint8_t* slot, int lane, int q) {
   return reinterpret_cast<uint4*>(slot + lane * 128 + ((q ^ (lane & 7)) << 4));
 }
 
-__device__ __forceinline__ void slot_store(const CUtensorMap* map, uint8_t* slot, int lane, int c0, int c1, int c2,
-                                           bool add) {
-  fence_proxy_async_smem();
+// Output of a warp's 32 rows through its two slots: put() each 128 bytes a row,
+// then send().  begin(): the slots may be written (their last stores have read
+// them).
+__device__ __forceinline__ void begin_out(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncwarp();
-  if (lane == 0) {
-    if (add) tma_add_3d(map, slot, c0, c1, c2);
-    else tma_store_3d(map, slot, c0, c1, c2);
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  }
 }
 
-// 64 values per lane (a row each) as bf16, through one of the warp's two slots: columns c0 .. c0+63 of rows c1 .. c1+31.
-__device__ __forceinline__ void emit_bf16x64(const CUtensorMap* map, uint8_t* slot, int lane, const float2* v, int c0,
-                                             int c1, int c2) {
-  slot_free(lane);
+// REST: v keeps what the written term leaves of the value.
+template <bool REST>
+__device__ __forceinline__ void put_bf16x64(uint8_t* slot, int lane, float2* v) {
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     uint4 pk;
@@ -246,20 +236,37 @@ __device__ __forceinline__ void emit_bf16x64(const CUtensorMap* map, uint8_t* sl
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 b2 = __float22bfloat162_rn(v[q * 4 + i]);
       w[i] = *reinterpret_cast<const uint32_t*>(&b2);
+      if constexpr (REST) {
+        v[q * 4 + i].x -= __uint_as_float(w[i] << 16);
+        v[q * 4 + i].y -= __uint_as_float(w[i] & 0xffff0000u);
+      }
     }
     *slot_piece(slot, lane, q) = pk;
   }
-  slot_store(map, slot, lane, c0, c1, c2, false);
 }
 
-__device__ __forceinline__ void emit_f32x32(const CUtensorMap* map, uint8_t* slot, int lane, const float2* v, int c0,
-                                            int c1, int c2, bool add) {
-  slot_free(lane);
+__device__ __forceinline__ void put_f32x32(uint8_t* slot, int lane, const float2* v) {
 #pragma unroll
   for (int q = 0; q < 8; ++q)
     *slot_piece(slot, lane, q) = make_uint4(__float_as_uint(v[2 * q].x), __float_as_uint(v[2 * q].y),
                                             __float_as_uint(v[2 * q + 1].x), __float_as_uint(v[2 * q + 1].y));
-  slot_store(map, slot, lane, c0, c1, c2, add);
+}
+
+// Slots 0 and (two) 1 to (c0, c1, c2) and dc0, dc2 further.
+__device__ __forceinline__ void send_out(const CUtensorMap* map, uint8_t* slots, int lane, int c0, int c1, int c2,
+                                         int dc0, int dc2, bool two, bool add) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (add) {
+      tma_add_3d(map, slots, c0, c1, c2);
+      if (two) tma_add_3d(map, slots + SLOT_BYTES, c0 + dc0, c1, c2 + dc2);
+    } else {
+      tma_store_3d(map, slots, c0, c1, c2);
+      if (two) tma_store_3d(map, slots + SLOT_BYTES, c0 + dc0, c1, c2 + dc2);
+    }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -292,8 +299,7 @@ __device__ __forceinline__ RowData load_row(const LossParams& p, int row, int nv
 template <int ROLE>
 __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps& maps, const Job& j, int nv,
                                             const RowData& rd, float2 (&sums)[64], int row_in_tile, int half,
-                                            int lane, uint8_t* slots, int& turn) {
-  auto slot = [&] { return slots + (turn ^= 1) * SLOT_BYTES; };
+                                            int lane, uint8_t* slots) {
   const int row = j.m0 + row_in_tile;
   const int wrow0 = row - lane;
   const int col0 = j.n0 + half * 128;
@@ -361,50 +367,41 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
       for (int i = 0; i < 64; ++i) sums[i] = make_float2(0.f, 0.f);
     }
     const int pc = col0 - p.v0;   // column in the piece
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (wrow0 >= p.n_rows || pc + 64 * h >= p.vc) continue;   // nothing of this box is in P
-      for (int t = 0; t < p.planes; ++t) {
-        emit_bf16x64(&maps.out0, slot(), lane, sums + 32 * h, 0, wrow0, t * p.panels + pc / 64 + h);
-        if (t + 1 < p.planes) {   // what the term just written leaves of the value
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float2 hi = __bfloat1622float2(__float22bfloat162_rn(sums[32 * h + i]));
-            sums[32 * h + i] = make_float2(sums[32 * h + i].x - hi.x, sums[32 * h + i].y - hi.y);
-          }
-        }
-      }
+    if (wrow0 >= p.n_rows || pc >= p.vc) return;   // nothing of these panels is in P
+    for (int t = 0; t + 1 < p.planes; ++t) {
+      begin_out(lane);
+      put_bf16x64<true>(slots, lane, sums);
+      put_bf16x64<true>(slots + SLOT_BYTES, lane, sums + 32);
+      send_out(&maps.out0, slots, lane, 0, wrow0, t * p.panels + pc / 64, 0, 1, pc + 64 < p.vc, false);
     }
+    begin_out(lane);
+    put_bf16x64<false>(slots, lane, sums);
+    put_bf16x64<false>(slots + SLOT_BYTES, lane, sums + 32);
+    send_out(&maps.out0, slots, lane, 0, wrow0, (p.planes - 1) * p.panels + pc / 64, 0, 1, pc + 64 < p.vc, false);
   } else {
-    if (j.dw) {
-      if (wrow0 >= p.vc) return;
-      if (p.dw_splits > 1) {
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-          if (col0 + 32 * h < p.d)
-            emit_f32x32(&maps.out0, slot(), lane, sums + 16 * h, col0 + 32 * h, wrow0, j.split, false);
-        return;
-      }
+    if (col0 >= p.d || wrow0 >= (j.dw ? p.vc : p.n_rows)) return;
+    const bool parts = !j.dw || p.dw_splits > 1;   // partial sums, joined by a later kernel
+    if (!parts) {
       const float f = *p.g_max * p.scale;
       const float2 f2 = make_float2(f, f);
 #pragma unroll
       for (int i = 0; i < 64; ++i) sums[i] = __fmul2_rn(sums[i], f2);
       if (p.dw_bf16) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (col0 + 64 * h < p.d) emit_bf16x64(&maps.out0, slot(), lane, sums + 32 * h, col0 + 64 * h, p.v0 + wrow0, 0);
-      } else {
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-          if (col0 + 32 * h < p.d)
-            emit_f32x32(&maps.out0, slot(), lane, sums + 16 * h, col0 + 32 * h, p.v0 + wrow0, 0, false);
+        begin_out(lane);
+        put_bf16x64<false>(slots, lane, sums);
+        put_bf16x64<false>(slots + SLOT_BYTES, lane, sums + 32);
+        send_out(&maps.out0, slots, lane, col0, p.v0 + wrow0, 0, 64, 0, col0 + 64 < p.d, false);
+        return;
       }
-    } else {
-      if (wrow0 >= p.n_rows) return;
+    }
 #pragma unroll
-      for (int h = 0; h < 4; ++h)
-        if (col0 + 32 * h < p.d)
-          emit_f32x32(&maps.out1, slot(), lane, sums + 16 * h, col0 + 32 * h, wrow0, j.split, p.dh_add != 0);
+    for (int h = 0; h < 2; ++h) {
+      if (col0 + 64 * h >= p.d) break;
+      begin_out(lane);
+      put_f32x32(slots, lane, sums + 32 * h);
+      put_f32x32(slots + SLOT_BYTES, lane, sums + 32 * h + 16);
+      send_out(j.dw ? &maps.out0 : &maps.out1, slots, lane, col0 + 64 * h, parts ? wrow0 : p.v0 + wrow0,
+               parts ? j.split : 0, 32, 0, col0 + 64 * h + 32 < p.d, !j.dw && p.dh_add);
     }
   }
 }
@@ -587,7 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     const int row_in_tile = (int)rank * 128 + quarter * 32 + lane;
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
     uint8_t* slots = smem + SM::SLOTS + (warp - 4) * 2 * SLOT_BYTES;
-    int buf = 0, turn = 0;
+    int buf = 0;
     uint32_t acc_phase = 0;
     bool ok = !skip;
     for (int t = cid; t < jobs.total && ok; t += ncl) {
@@ -632,7 +629,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
         if (++buf == 2) { buf = 0; acc_phase ^= 1; }
       }
-      if (ok) finish_tile<ROLE>(p, maps, j, nv, rd, acc, row_in_tile, half, lane, slots, turn);
+      if (ok) finish_tile<ROLE>(p, maps, j, nv, rd, acc, row_in_tile, half, lane, slots);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
