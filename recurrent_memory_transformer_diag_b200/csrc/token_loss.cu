@@ -1059,7 +1059,7 @@ struct RowParams {
   int twice;                  // few bf16 rows: rows 0 .. twice-1, zeros behind the last, and the same again
   const void* targets; int target_bytes;
   const void* hidden;
-  bf16* rows;                 // [planes][n][d]
+  bf16* rows; int pitch;      // [planes][n][pitch]
   int* perm; int* target; int* n_valid;
   const int2* counts;         // many rows: rows with a target and the largest |weight| (its bits) of every 1024 rows
   // gradient: weights divided by the largest magnitude (so that a weight that
@@ -1185,7 +1185,7 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
   }
   __syncthreads();
   const int vecs = p.d / 8;   // 8 elements per step, four steps in flight
-  const long long plane = (long long)p.n * p.d;
+  const long long plane = (long long)p.n * p.pitch;
   const T* src = reinterpret_cast<const T*>(p.hidden) + (long long)r0 * p.d;
   for (int k0 = threadIdx.x; k0 < nr * vecs; k0 += 4 * 256) {
     Vec8<T> x[4];
@@ -1201,10 +1201,10 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
       if (k >= nr * vecs) continue;
       const int r = k / vecs, c = (k - r * vecs) * 8;
       const int at = s_slot[r] >= 0 ? s_slot[r] : ~s_slot[r];
-      bf16* dst = p.rows + (long long)at * p.d + c;
+      bf16* dst = p.rows + (long long)at * p.pitch + c;
       if constexpr (sizeof(T) == 2) {
         x[u].store(dst);
-        if (p.twice) x[u].store(dst + (long long)p.twice * p.d);
+        if (p.twice) x[u].store(dst + (long long)p.twice * p.pitch);
       } else {
         float f[8];
         x[u].get(f);
@@ -1218,14 +1218,23 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
   }
 }
 
-// fp32 head as three bf16 terms: out[3][n], n a multiple of 8.
-__global__ void __launch_bounds__(256) split_terms_kernel(const float* x, bf16* out, long long n) {
-  for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (long long)gridDim.x * 256 * 8) {
+// fp32 head as three bf16 terms, out[3][rows][pitch]: n groups of 8 columns, vecs a row.
+__global__ void __launch_bounds__(256) split_terms_kernel(const float* x, bf16* out, long long n, int vecs,
+                                                          int pitch) {
+  const long long plane = n / vecs * pitch;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+    const long long r = i / vecs;
+    const int c = (int)(i - r * vecs) * 8;
+    Vec8<float> v;
+    v.load(x + i * 8);
+    float f[8];
+    v.get(f);
     __align__(16) bf16 t[3][8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) split3(x[i + k], t[0][k], t[1][k], t[2][k]);
+    for (int k = 0; k < 8; ++k) split3(f[k], t[0][k], t[1][k], t[2][k]);
 #pragma unroll
-    for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(out + q * n + i) = *reinterpret_cast<uint4*>(t[q]);
+    for (int q = 0; q < 3; ++q)
+      *reinterpret_cast<uint4*>(out + q * plane + r * pitch + c) = *reinterpret_cast<uint4*>(t[q]);
   }
 }
 
@@ -1300,7 +1309,7 @@ __global__ void __launch_bounds__(1024) join_lse_kernel(const JoinParams p) {
 // groups of splits side by side, 1024 / G columns a block and step.  After a
 // wait that ran out: NaN here and in all of `head`, where that is given.
 struct JoinRows {
-  const float* part; int splits, rows, two_terms, n, d;
+  const float* part; int splits, rows, pitch, two_terms, n, d;
   const int* perm; const int* n_valid;
   const float* g_max; float scale;
   const unsigned* err;
@@ -1321,7 +1330,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const JoinRows p) {
   const int nv = p.perm ? *p.n_valid : p.n;
   const float f = *p.g_max * p.scale;
   const int vecs = p.d / 4, per = (p.splits + G - 1) / G;
-  const long long total = (long long)p.n * vecs, plane = (long long)p.rows * p.d;
+  const long long total = (long long)p.n * vecs, plane = (long long)p.rows * p.pitch;
   for (long long k0 = (long long)blockIdx.x * X; k0 < total; k0 += (long long)gridDim.x * X) {
     const long long k = k0 + x;
     const int r = (int)(k / vecs), c = (int)(k - (long long)r * vecs) * 4;
@@ -1330,9 +1339,9 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const JoinRows p) {
     if (k < total && r < nv) {
 #pragma unroll 4
       for (int i = y * per; i < min(p.splits, (y + 1) * per); ++i) {
-        const float* at = p.part + i * plane + (long long)r * p.d + c;
+        const float* at = p.part + i * plane + (long long)r * p.pitch + c;
         add(*reinterpret_cast<const float4*>(at));
-        if (p.two_terms) add(*reinterpret_cast<const float4*>(at + (long long)p.two_terms * p.d));
+        if (p.two_terms) add(*reinterpret_cast<const float4*>(at + (long long)p.two_terms * p.pitch));
       }
     }
     if constexpr (G > 1) {
@@ -1383,10 +1392,12 @@ int few_cols(int n) { return n <= 16 ? 16 : FEW_ROWS; }
 
 // Workspace of one call, laid out in order.
 struct Layout {
-  int planes, rows, g_rows, two_terms, pieces, vc, splits, k_split, dw_splits, dw_k, n_parts;
+  int planes, dp, dq, rows, g_rows, two_terms, pieces, vc, splits, k_split, dw_splits, dw_k, n_parts;
   size_t block_err, counts, n_valid, g_max, rows_b, perm, target, g, lse, tlogit, part, head, p, dh, dw, total;
   Layout(int n, int v, int d, bool f32, bool grad) {
     planes = f32 ? 3 : 1;
+    dp = round_up(d, 64);   // rows kept here start on 128-byte lines: a copied box row is one line, not two
+    dq = round_up(d, 32);   // (d = 1032 against 1024: 181 and 135 us with rows and head off the lines)
     // P beside bf16 operands is one bf16 term; for few rows two (few roundings do
     // not average out, and the products are not what bounds the gradient): the
     // second terms stand as further rows of P, beside the same hidden rows again
@@ -1427,17 +1438,17 @@ struct Layout {
     counts = take(rows > COUNTED_FROM ? (size_t)div_up(rows, COUNT_ROWS) * 8 : 0);
     n_valid = take(4);
     g_max = take(4);
-    rows_b = take((size_t)planes * (grad ? g_rows : rows) * d * 2);
+    rows_b = take((size_t)planes * (grad ? g_rows : rows) * dp * 2);
     perm = take((size_t)rows * 4);
     target = take((size_t)rows * 4);
     g = take(grad ? (size_t)rows * 4 : 0);
     lse = take(grad ? (size_t)rows * 4 : 0);
     tlogit = take(grad ? 0 : (size_t)rows * 4);
     part = take(grad ? 0 : (size_t)n_parts * rows * 8);
-    head = take(f32 && !simt ? (size_t)3 * v * d * 2 : 0);
+    head = take(f32 && !simt ? (size_t)3 * v * dp * 2 : 0);
     p = take(grad ? (size_t)planes * (two_terms ? g_rows : (n <= FEW_ROWS ? few_cols(n) : n)) * round_up(vc, 64) * 2 : 0);
-    dh = take(grad ? (size_t)splits * g_rows * d * 4 : 0);
-    dw = take(dw_splits > 1 ? (size_t)dw_splits * vc * d * 4 : 0);
+    dh = take(grad ? (size_t)splits * g_rows * dq * 4 : 0);
+    dw = take(dw_splits > 1 ? (size_t)dw_splits * vc * dq * 4 : 0);
     total = o;
   }
 };
@@ -1520,13 +1531,13 @@ cudaError_t launch_f32_few(const LossParams& p, const void* hidden, const void* 
 int few_chunk(int n) { return n <= 16 ? 2 : 4; }
 
 // The head as the few-rows kernel reads it: boxes of 32 entries.
-cudaError_t few_head_map(CUtensorMap* map, const void* head, int v, int d, int planes) {
-  return make_map(map, head, false, d, d, v, planes, BK, 32);
+cudaError_t few_head_map(CUtensorMap* map, const void* head, int v, int d, int pitch, int planes) {
+  return make_map(map, head, false, d, pitch, v, planes, BK, 32);
 }
 
 // Hidden rows as the few-rows kernel reads them: boxes of NT rows.
-cudaError_t few_map(CUtensorMap* map, const void* rows, int n, int d, int planes) {
-  return make_map(map, rows, false, d, d, n, planes, BK, n <= 16 ? 16 : FEW_ROWS);
+cudaError_t few_map(CUtensorMap* map, const void* rows, int n, int d, int pitch, int planes) {
+  return make_map(map, rows, false, d, pitch, n, planes, BK, n <= 16 ? 16 : FEW_ROWS);
 }
 
 template <int ROLE>
@@ -1569,10 +1580,9 @@ cudaError_t head_operand(const Layout& L, char* ws, const void* head, int v, int
                          cudaStream_t st) {
   *out = head;
   if (!f32) return cudaSuccess;
-  const long long n = (long long)v * d;
-  const long long blocks = (n / 8 + 255) / 256;
+  const long long n = (long long)v * (d / 8), blocks = (n + 255) / 256;
   split_terms_kernel<<<(int)(blocks < 148 * 16 ? blocks : 148 * 16), 256, 0, st>>>((const float*)head,
-                                                                                (bf16*)(ws + L.head), n);
+                                                                                (bf16*)(ws + L.head), n, d / 8, L.dp);
   *out = ws + L.head;
   return cudaGetLastError();
 }
@@ -1637,8 +1647,8 @@ extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d
       e = n <= 4 ? launch_f32_few<4>(p, hidden, head, st) : launch_f32_few<F32_FEW_ROWS>(p, hidden, head, st);
     } else {
       jp.blocks = few_blocks(vocab);
-      e = few_map(&maps.a, hidden, n, d, 1);
-      if (e == cudaSuccess) e = few_head_map(&maps.b, head, vocab, d, 1);
+      e = few_map(&maps.a, hidden, n, d, d, 1);
+      if (e == cudaSuccess) e = few_head_map(&maps.b, head, vocab, d, d, 1);
       if (e == cudaSuccess) e = n <= 16 ? launch_few<LSE, 16>(maps, p, st) : launch_few<LSE, 64>(maps, p, st);
     }
     if (e == cudaSuccess) e = join(n, 0);
@@ -1647,20 +1657,22 @@ extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d
   const void* w = nullptr;
   cudaError_t e = head_operand(L, ws, head, vocab, d, f32, &w, st);
   const bool few = n <= FEW_ROWS;   // up to 64 rows: bound by reading the head
+  const int wp = f32 ? L.dp : d;
   if (e == cudaSuccess)
-    e = few ? few_head_map(&maps.b, w, vocab, d, L.planes) : load_map(&maps.b, w, d, d, vocab, L.planes);
+    e = few ? few_head_map(&maps.b, w, vocab, d, wp, L.planes) : load_map(&maps.b, w, d, wp, vocab, L.planes);
   for (int r0 = 0; r0 < n && e == cudaSuccess; r0 += L.rows) {
     const int nr = n - r0 < L.rows ? n - r0 : L.rows;
     RowParams rp{};
     rp.n = nr; rp.d = d; rp.vocab = vocab; rp.clear_err = r0 == 0;
     rp.targets = (const char*)targets + (size_t)r0 * target_bytes; rp.target_bytes = target_bytes;
     rp.hidden = (const char*)hidden + (size_t)r0 * d * (f32 ? 4 : 2);
-    rp.rows = (bf16*)(ws + L.rows_b); rp.perm = (int*)(ws + L.perm); rp.target = (int*)(ws + L.target);
+    rp.rows = (bf16*)(ws + L.rows_b); rp.pitch = L.dp; rp.perm = (int*)(ws + L.perm); rp.target = (int*)(ws + L.target);
     rp.n_valid = (int*)(ws + L.n_valid); rp.err = (unsigned*)ws;
     rp.loss_out = loss + r0; rp.lse_out = lse + r0;
     e = launch_order_rows(rp, f32, (int2*)(ws + L.counts), st);
     if (e == cudaSuccess)
-      e = few ? few_map(&maps.a, ws + L.rows_b, nr, d, L.planes) : load_map(&maps.a, ws + L.rows_b, d, d, nr, L.planes);
+      e = few ? few_map(&maps.a, ws + L.rows_b, nr, d, L.dp, L.planes)
+              : load_map(&maps.a, ws + L.rows_b, d, L.dp, nr, L.planes);
     if (e != cudaSuccess) break;
     p.n_rows = p.part_pitch = nr;
     p.n_valid = jp.n_valid = rp.n_valid;
@@ -1694,29 +1706,30 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
   RowParams rp{};
   rp.n = n; rp.d = d; rp.vocab = vocab; rp.clear_err = 1;
   rp.targets = targets; rp.target_bytes = target_bytes; rp.hidden = hidden;
-  rp.rows = (bf16*)(ws + L.rows_b); rp.perm = (int*)(ws + L.perm); rp.target = (int*)(ws + L.target);
+  rp.rows = (bf16*)(ws + L.rows_b); rp.pitch = L.dp; rp.perm = (int*)(ws + L.perm); rp.target = (int*)(ws + L.target);
   rp.n_valid = (int*)(ws + L.n_valid); rp.err = (unsigned*)ws;
   rp.twice = L.two_terms;
   rp.d_loss = d_loss; rp.lse_in = lse; rp.g = (float*)(ws + L.g); rp.lse = (float*)(ws + L.lse);
   rp.g_max = (float*)(ws + L.g_max);
   if (e == cudaSuccess) e = launch_order_rows(rp, f32, (int2*)(ws + L.counts), st);
+  const int wp = f32 ? L.dp : d;
   LossMaps mp{}, mg{};   // PROB, GRAD
-  if (e == cudaSuccess) e = load_map(&mp.a, ws + L.rows_b, d, d, L.g_rows, L.planes);
-  if (e == cudaSuccess) e = load_map(&mp.b, w, d, d, vocab, L.planes);
+  if (e == cudaSuccess) e = load_map(&mp.a, ws + L.rows_b, d, L.dp, L.g_rows, L.planes);
+  if (e == cudaSuccess) e = load_map(&mp.b, w, d, wp, vocab, L.planes);
   mg.b = mp.b;
   mg.c = mp.a;
   if (e == cudaSuccess && d_head)
-    e = L.dw_splits > 1 ? make_map(&mg.out0, ws + L.dw, true, d, d, L.vc, L.dw_splits, 32, 32)
+    e = L.dw_splits > 1 ? make_map(&mg.out0, ws + L.dw, true, d, L.dq, L.vc, L.dw_splits, 32, 32)
                         : make_map(&mg.out0, d_head, f32, d, d, vocab, 1, f32 ? 32 : 64, 32);
-  if (e == cudaSuccess && d_hidden) e = make_map(&mg.out1, ws + L.dh, true, d, d, L.g_rows, L.splits, 32, 32);
+  if (e == cudaSuccess && d_hidden) e = make_map(&mg.out1, ws + L.dh, true, d, L.dq, L.g_rows, L.splits, 32, 32);
   LossParams p{};
   p.n_rows = n; p.d = d; p.vocab = vocab; p.planes = L.planes; p.scale = scale;
   p.n_valid = rp.n_valid; p.target = rp.target; p.lse = rp.lse; p.g = rp.g; p.g_max = rp.g_max; p.err = rp.err;
   p.want_dw = d_head != nullptr; p.want_dh = d_hidden != nullptr; p.dw_bf16 = !f32; p.k_split = L.k_split;
   p.dw_splits = L.dw_splits; p.dw_k = L.dw_k;
   const bool few = n <= FEW_ROWS;
-  if (e == cudaSuccess && few) e = few_map(&mp.a, ws + L.rows_b, n, d, L.planes);
-  if (e == cudaSuccess && few) e = few_head_map(&mp.b, w, vocab, d, L.planes);
+  if (e == cudaSuccess && few) e = few_map(&mp.a, ws + L.rows_b, n, d, L.dp, L.planes);
+  if (e == cudaSuccess && few) e = few_head_map(&mp.b, w, vocab, d, wp, L.planes);
   const int mt = div_up(L.g_rows, TILE), dt = div_up(d, TILE);
   for (int v0 = 0; v0 < vocab && e == cudaSuccess; v0 += L.vc) {
     p.v0 = v0;
@@ -1742,7 +1755,7 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     if (e == cudaSuccess) e = launch_products<GRAD>(mg, pg, jobs, st);
     if (e == cudaSuccess && d_head && L.dw_splits > 1) {
       JoinRows jr{};
-      jr.part = (const float*)(ws + L.dw); jr.splits = L.dw_splits; jr.rows = L.vc; jr.n = p.vc; jr.d = d;
+      jr.part = (const float*)(ws + L.dw); jr.splits = L.dw_splits; jr.rows = L.vc; jr.pitch = L.dq; jr.n = p.vc; jr.d = d;
       jr.g_max = rp.g_max; jr.scale = scale; jr.err = rp.err;
       jr.out = (char*)d_head + (size_t)v0 * d * (f32 ? 4 : 2);
       e = launch_join_rows(jr, f32, st);
@@ -1750,7 +1763,7 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
   }
   if (e == cudaSuccess) {
     JoinRows jr{};
-    jr.part = (const float*)(ws + L.dh); jr.splits = L.splits; jr.rows = L.g_rows; jr.two_terms = L.two_terms;
+    jr.part = (const float*)(ws + L.dh); jr.splits = L.splits; jr.rows = L.g_rows; jr.pitch = L.dq; jr.two_terms = L.two_terms;
     jr.n = n; jr.d = d; jr.perm = rp.perm; jr.n_valid = rp.n_valid; jr.g_max = rp.g_max; jr.scale = scale;
     jr.err = rp.err; jr.out = d_hidden; jr.head = d_head; jr.head_n = (long long)vocab * d;
     e = launch_join_rows(jr, f32, st);
