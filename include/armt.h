@@ -415,6 +415,13 @@ armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, int d, cons
  * (ARMT_ERR_DEVICE_TIMEOUT; its results are NaN then), ARMT_OK otherwise. */
 armt_status armt_workspace_status(const void* workspace, void* stream);
 
+/* Test hook for failure detection, as armt_test_bounded_wait: an
+ * armt_token_loss of `rows` rows with its copies never issued.  Returns
+ * ARMT_ERR_DEVICE_TIMEOUT when the waits ran out and the loss came back as NaN
+ * (the expected result), ARMT_OK otherwise, or the error of a call.
+ * Synchronous on stream; allocates its own small buffers. */
+armt_status armt_test_loss_wait(int rows, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -37,7 +37,7 @@ EXPORTS = (
     "armt_forward_ex", "armt_test_bounded_wait", "armt_stage_wave",
     "armt_embed", "armt_embed_grad", "armt_embed_grad_workspace", "armt_rms_norm", "armt_rms_norm_grad",
     "armt_rms_norm_grad_workspace", "armt_token_loss", "armt_token_loss_grad", "armt_token_loss_workspace",
-    "armt_workspace_status",
+    "armt_workspace_status", "armt_test_loss_wait",
 )
 
 
@@ -114,6 +114,7 @@ def lib() -> ctypes.CDLL:
     L.armt_token_loss.argtypes = [c_int] * 4 + [vp, vp, vp, c_int, c_float, vp, vp, vp, c_size, vp]
     L.armt_token_loss_grad.argtypes = [c_int] * 4 + [vp, vp, vp, c_int, c_float] + [vp] * 5 + [c_size, vp]
     L.armt_workspace_status.argtypes = [vp, vp]
+    L.armt_test_loss_wait.argtypes = [c_int, vp]
     for name in EXPORTS:
         if name not in ("armt_status_string", "armt_last_error", "armt_kernel_kind_name"):
             getattr(L, name).restype = c_int

@@ -99,6 +99,7 @@ struct LossParams {
   int dw_splits, dw_k;        // dW's contraction in splits of dw_k rows, as partial sums where there are several
   const float* g_max;
   unsigned* err;
+  int debug_no_loads;         // test hook: no copies are issued, so the first wait for a stage runs out
 };
 
 struct LossMaps {
@@ -493,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
         armed &= ~(1u << stage);
         uint8_t* sa = smem + stage * STAGE_BYTES;
-        if (issuer) {
+        if (issuer && !p.debug_no_loads) {
           const int ta = term_a(q, products), tb = term_b(q, products);
           // both CTAs' copies
           if (leader) mbar_expect_tx(&full[stage], 2 * (2 * BOX_BYTES + j.n / 128 * BOX_BYTES));
@@ -766,7 +767,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
         armed &= ~(1u << stage);
         uint8_t* sa = smem + stage * SM::STAGE;
-        if (issuer) {
+        if (issuer && !p.debug_no_loads) {
           const int ta = term_a(q, products), tb = term_b(q, products);
           mbar_expect_tx(&full[stage], boxes * (BOX_BYTES / 2) + SM::H_BYTES);
           for (int h = 0; h < boxes; ++h)
@@ -1397,7 +1398,7 @@ struct Layout {
   Layout(int n, int v, int d, bool f32, bool grad) {
     planes = f32 ? 3 : 1;
     dp = round_up(d, 64);   // rows kept here start on 128-byte lines: a copied box row is one line, not two
-    dq = round_up(d, 32);   // (d = 1032 against 1024: 181 and 135 us with rows and head off the lines)
+    dq = round_up(d, 32);   // (834 rows, 96794 x 1032: 181 us off the lines, 156 on them)
     // P beside bf16 operands is one bf16 term; for few rows two (few roundings do
     // not average out, and the products are not what bounds the gradient): the
     // second terms stand as further rows of P, beside the same hidden rows again
@@ -1603,9 +1604,9 @@ extern "C" armt_status armt_token_loss_workspace(armt_dtype dtype, int n, int vo
   return ARMT_OK;
 }
 
-extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d, const void* hidden, const void* head,
-                                       const void* targets, int target_bytes, float scale, float* loss, float* lse,
-                                       void* workspace, size_t workspace_bytes, void* stream) {
+static armt_status token_loss(armt_dtype dtype, int n, int vocab, int d, const void* hidden, const void* head,
+                              const void* targets, int target_bytes, float scale, float* loss, float* lse,
+                              void* workspace, size_t workspace_bytes, void* stream, int debug_no_loads) {
   armt_status s = check_sizes(dtype, n, vocab, d);
   if (s != ARMT_OK) return s;
   if (!hidden || !head || !targets || !loss || !lse || !workspace || !std::isfinite(scale) ||
@@ -1621,6 +1622,7 @@ extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d
   jp.err = (unsigned*)ws; jp.vocab = vocab;
   LossParams p{};
   p.d = d; p.vocab = vocab; p.planes = L.planes; p.v0 = 0; p.vc = vocab; p.scale = scale;
+  p.debug_no_loads = debug_no_loads;
   p.part = (float2*)(ws + L.part); p.target_logit = (float*)(ws + L.tlogit); p.err = (unsigned*)ws;
   auto join = [&](int rows, int r0) {
     jp.rb = 32;
@@ -1684,6 +1686,13 @@ extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d
     if (e == cudaSuccess) e = join(nr, r0);
   }
   return cuda_status(e);
+}
+
+extern "C" armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d, const void* hidden, const void* head,
+                                       const void* targets, int target_bytes, float scale, float* loss, float* lse,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  return token_loss(dtype, n, vocab, d, hidden, head, targets, target_bytes, scale, loss, lse, workspace,
+                    workspace_bytes, stream, 0);
 }
 
 extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, int d, const void* hidden,
@@ -1780,4 +1789,34 @@ extern "C" armt_status armt_workspace_status(const void* workspace, void* stream
   if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_status(e);
   return err ? ARMT_ERR_DEVICE_TIMEOUT : ARMT_OK;
+}
+
+// The bounded-wait error path on demand: a loss of `rows` zero rows (16 k-blocks,
+// more than the stages) whose copies are never issued.  Every wait of the
+// products then runs out (about one second), the blocks leave and free their
+// tensor memory, the join finds the error and writes NaN.
+extern "C" armt_status armt_test_loss_wait(int rows, void* stream) {
+  const int v = 600, d = 1024;
+  size_t need = 0;
+  armt_status s = armt_token_loss_workspace(ARMT_BF16, rows, v, d, 0, &need);
+  if (s != ARMT_OK) return s;
+  cudaStream_t st = (cudaStream_t)stream;
+  const size_t data = ((size_t)rows + v) * d * 2 + (size_t)rows * 16 + 1024;
+  char* buf = nullptr;
+  cudaError_t e = cudaMallocAsync((void**)&buf, data + need, st);
+  if (e != cudaSuccess) return cuda_status(e);
+  char* hidden = buf + need;
+  char* head = hidden + (size_t)rows * d * 2;
+  char* targets = head + (size_t)v * d * 2;
+  float* loss = (float*)(targets + (size_t)rows * 8);
+  float host = 0.f;
+  e = cudaMemsetAsync(buf, 0, data + need, st);
+  s = cuda_status(e);
+  if (s == ARMT_OK)
+    s = token_loss(ARMT_BF16, rows, v, d, hidden, head, targets, 8, 1.f, loss, loss + rows, buf, need, stream, 1);
+  if (s == ARMT_OK) s = cuda_status(cudaMemcpyAsync(&host, loss, sizeof(float), cudaMemcpyDeviceToHost, st));
+  if (s == ARMT_OK) s = armt_workspace_status(buf, stream);   // waits for the stream
+  if (s == ARMT_ERR_DEVICE_TIMEOUT && !std::isnan(host)) s = ARMT_OK;
+  cudaFreeAsync(buf, st);
+  return s;
 }

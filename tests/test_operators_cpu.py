@@ -83,6 +83,7 @@ def test_refusals(libarmt, name, base, change, status):
 
 def test_status_of_no_workspace(libarmt):
     assert libarmt.armt_workspace_status(None, None) == INVALID
+    assert libarmt.armt_test_loss_wait(0, None) == INVALID
 
 
 def test_wrappers_refuse_tensors_off_the_device():

@@ -581,6 +581,19 @@ def test_score_runs_ids_to_losses(name):
         assert torch.equal(torch.cat(parts), loss)
 
 
+@pytest.mark.parametrize("rows", [4, 40, 200])
+def test_bounded_waits_of_the_loss(rows):
+    """Copies that never come: the waits run out after about a second, the status and a
+    NaN loss say so, and the next call (in this process, on this device) is right."""
+    import time
+    from recurrent_memory_transformer_diag_b200.armt import STATUS, lib
+    t0 = time.time()
+    status = lib().armt_test_loss_wait(rows, torch.cuda.current_stream().cuda_stream)
+    assert STATUS[status] == "ARMT_ERR_DEVICE_TIMEOUT" and time.time() - t0 < 20
+    hidden, head, t, w = loss_inputs(rows, rows, 700, 128, BF)
+    check_loss(hidden, head, t, w, 1.0, run_loss(hidden, head, t, w))
+
+
 # ------------------------------------------------------------------ refusals
 def _refusals():
     z = lambda *s, dt=BF: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
