@@ -27,9 +27,11 @@
 // bf16 right away (P and the gradients of bf16 operands) takes one accumulator
 // over the whole contraction.
 //
-// fp32 operands: x = hi + mid + lo with three bf16 terms (24 bits), and the six
-// products hi lo, lo hi, mid mid, hi mid, mid hi, hi hi run one after another
-// into the same sums; the dropped ones are below 2^-24 of the result.
+// fp32 operands: x = hi + mid + lo with three bf16 terms (24 bits).  A k-block
+// is three stages, one for each term of both operands, and six products into
+// the same sums: every pair of terms but the three whose product is below
+// 2^-24 of the result.  (Six copies of two tiles instead took 437 ns a product
+// of a 256 x 256 tile, against 270 for the product itself.)
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -73,7 +75,7 @@ struct Smem {
 constexpr int ROW_GROUP = 32;          // row tiles that share a vocabulary tile before the next one
 constexpr int LSE_CHUNK = 8;           // k-blocks per accumulator of the loss's logits (K = 512)
 constexpr int WHOLE_CHUNK = 1 << 16;   // ... of what is rounded to bf16 (K = 4 M: well inside the bounded waits)
-constexpr int F32_CHUNK = 4;           // ... of everything that fp32 operands give (K = 256)
+constexpr int F32_CHUNK = 1;           // ... of everything that fp32 operands give (six products of K = 64)
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct LossParams {
@@ -106,16 +108,6 @@ struct LossMaps {
   CUtensorMap a, b, c;        // operands: LSE/PROB hidden, head; GRAD P, head, hidden
   CUtensorMap out0, out1;     // PROB: P; GRAD: dW, dH partial sums
 };
-
-// Products of a tile, and the terms that product q of fp32 operands multiplies
-// (smallest products first).
-__device__ __forceinline__ int n_products(int planes) { return planes == 3 ? 6 : 1; }
-__device__ __forceinline__ int term_a(int q, int products) {
-  return products == 6 ? (0x021010 >> (4 * (5 - q))) & 15 : 0;
-}
-__device__ __forceinline__ int term_b(int q, int products) {
-  return products == 6 ? (0x201100 >> (4 * (5 - q))) & 15 : 0;
-}
 
 // One tile of work: D[256 x 256] = A B^T over k-blocks kb = 0 .. kblocks-1.
 struct Job {
@@ -469,7 +461,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 
   const int nv = ROLE == GRAD && p.two_terms ? 2 * p.two_terms : *p.n_valid;
   const Jobs<ROLE> jobs(p, nv);
-  const int products = n_products(p.planes);
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
 
   if (warp < 4) {
@@ -489,13 +480,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const CUtensorMap* ma = &maps.a;
       const CUtensorMap* mb = ROLE == GRAD && j.dw ? &maps.c : &maps.b;
       const int am = j.m0 + (int)rank * 128, bn = j.n0 + (int)rank * (j.n / 2);
-      // the products of a k-block one after another: its tiles come from L2 again
-      for (int kb = 0, q = 0; kb < j.kblocks;) {
+      for (int kb = 0, q = 0; kb < j.kblocks;) {   // q: the term of both operands
         if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
         armed &= ~(1u << stage);
         uint8_t* sa = smem + stage * STAGE_BYTES;
         if (issuer && !p.debug_no_loads) {
-          const int ta = term_a(q, products), tb = term_b(q, products);
           // both CTAs' copies
           if (leader) mbar_expect_tx(&full[stage], 2 * (2 * BOX_BYTES + j.n / 128 * BOX_BYTES));
           const uint32_t fb = full0 + (uint32_t)(stage * sizeof(uint64_t));
@@ -504,17 +493,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           for (int h = 0; h < 2; ++h) {
             const int row = am + 64 * h;
             if (ROLE == GRAD && !p.p_trans)
-              tma_load_3d_pair(ma, fb, sa + h * BOX_BYTES, 0, a_mn ? ka : row, ta * p.panels + (a_mn ? row : ka) / BK);
+              tma_load_3d_pair(ma, fb, sa + h * BOX_BYTES, 0, a_mn ? ka : row, q * p.panels + (a_mn ? row : ka) / BK);
             else
-              tma_load_3d_pair(ma, fb, sa + h * BOX_BYTES, a_mn ? row : ka, a_mn ? ka : row, ta);
+              tma_load_3d_pair(ma, fb, sa + h * BOX_BYTES, a_mn ? row : ka, a_mn ? ka : row, q);
             if (128 * h < j.n)
               tma_load_3d_pair(mb, fb, sa + (2 + h) * BOX_BYTES, b_mn ? bn + 64 * h : kbb, b_mn ? kbb : bn + 64 * h,
-                               tb);
+                               q);
           }
         }
         armed |= 1u << stage;
         if (++stage == STAGES) { stage = 0; phase ^= 1; }
-        if (++q == products) { q = 0; ++kb; }
+        if (++q == p.planes) { q = 0; ++kb; }
       }
     }
     if (!ok) {
@@ -542,24 +531,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         const bool a_mn = ROLE == GRAD && j.dw != (p.p_trans != 0), b_mn = ROLE == GRAD;
         const uint32_t idesc = idesc_f16(j.n, 1, TILE) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
         const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
-        const int iters = products * j.kblocks;
-        for (int it = 0; it < iters && ok;) {
+        for (int it = 0; it < j.kblocks && ok;) {
           if (!mbar_wait_cluster_warp(&tempty[buf], acc_phase ^ 1, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + (uint32_t)(buf * TILE);
-          const int end = min(iters, it + p.chunk);
-          for (int first = it; it < end; ++it) {
-            if (!mbar_wait_cluster_warp(&full[stage], phase, abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
-            const uint32_t sb = sa + 2 * BOX_BYTES;
+          const int end = min(j.kblocks, it + p.chunk);
+          auto product = [&](int sa, int sb, bool add) {   // of the A tile of one stage and the B tile of another
+            const uint32_t a = smem_u32(smem + sa * STAGE_BYTES), b = smem_u32(smem + sb * STAGE_BYTES) + 2 * BOX_BYTES;
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
-              if (issuer)
-                mma_f16_pair(d_tmem, operand_desc(sa + kk * step_a, a_mn), operand_desc(sb + kk * step_b, b_mn), idesc,
-                             (it > first || kk > 0) ? 1u : 0u);
-            if (issuer) mma_commit_pair(&empty[stage], 0x3);
-            if (++stage == STAGES) { stage = 0; phase ^= 1; }
+              mma_f16_pair(d_tmem, operand_desc(a + kk * step_a, a_mn), operand_desc(b + kk * step_b, b_mn), idesc,
+                           (add || kk > 0) ? 1u : 0u);
+          };
+          for (int first = it; it < end && ok; ++it) {
+            int s0 = stage, s1 = stage;   // stages of the first two terms
+            for (int q = 0; q < p.planes; ++q) {
+              if (!mbar_wait_cluster_warp(&full[stage], phase, abort_flag)) { ok = false; break; }
+              tc_fence_after();
+              if (q == 1) s1 = stage;
+              if (issuer) {
+                if (q == 0) {
+                  product(s0, s0, it > first);
+                } else if (q == 1) {
+                  product(s0, s1, true);
+                  product(s1, s0, true);
+                  product(s1, s1, true);
+                  mma_commit_pair(&empty[s1], 0x3);
+                } else {
+                  product(s0, stage, true);
+                  product(stage, s0, true);
+                  mma_commit_pair(&empty[stage], 0x3);
+                }
+                if (q == p.planes - 1) mma_commit_pair(&empty[s0], 0x3);
+              }
+              if (++stage == STAGES) { stage = 0; phase ^= 1; }
+            }
           }
           if (!ok) break;
           if (issuer) mma_commit_pair(&tfull[buf], 0x3);
@@ -596,8 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
       }
-      const int iters = products * j.kblocks;
-      for (int it = 0; it < iters; it += p.chunk) {
+      for (int it = 0; it < j.kblocks; it += p.chunk) {
         const bool got = mbar_wait_cluster(&tfull[buf], acc_phase, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
           if (lane == 0) atomicOr(p.err, 4u);
@@ -749,8 +754,6 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int kblocks = (p.d + BK - 1) / BK;
-  const int products = n_products(p.planes);
-  const int iters = products * kblocks;
   // the CTA's entries: as even as 32 rows (a box) allow
   const int per = few_range(p.vc);
   const int v0 = min((int)blockIdx.x * per, p.vc);
@@ -768,15 +771,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         armed &= ~(1u << stage);
         uint8_t* sa = smem + stage * SM::STAGE;
         if (issuer && !p.debug_no_loads) {
-          const int ta = term_a(q, products), tb = term_b(q, products);
           mbar_expect_tx(&full[stage], boxes * (BOX_BYTES / 2) + SM::H_BYTES);
           for (int h = 0; h < boxes; ++h)
-            tma_load_3d(&maps.b, &full[stage], sa + h * (BOX_BYTES / 2), kb * BK, v + 32 * h, tb);
-          tma_load_3d(&maps.a, &full[stage], sa + 2 * BOX_BYTES, kb * BK, 0, ta);
+            tma_load_3d(&maps.b, &full[stage], sa + h * (BOX_BYTES / 2), kb * BK, v + 32 * h, q);
+          tma_load_3d(&maps.a, &full[stage], sa + 2 * BOX_BYTES, kb * BK, 0, q);
         }
         armed |= 1u << stage;
         if (++stage == SM::N_STAGES) { stage = 0; phase ^= 1; }
-        if (++q == products) { q = 0; ++kb; }
+        if (++q == p.planes) { q = 0; ++kb; }
       }
     }
     if (!ok) {
@@ -799,22 +801,40 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
     for (int t = v0; t < v1 && ok; t += 128) {
-      for (int it = 0; it < iters && ok;) {
+      for (int it = 0; it < kblocks && ok;) {
         if (!mbar_wait_warp(&tempty[buf], acc_phase ^ 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(buf * NT);
-        const int end = min(iters, it + p.chunk);
-        for (int first = it; it < end; ++it) {
-          if (!mbar_wait_warp(&full[stage], phase, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * SM::STAGE);
+        const int end = min(kblocks, it + p.chunk);
+        auto product = [&](int sa, int sb, bool add) {   // of the head tile of one stage and the rows of another
+          const uint32_t a = smem_u32(smem + sa * SM::STAGE), b = smem_u32(smem + sb * SM::STAGE) + 2 * BOX_BYTES;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            if (issuer)
-              mma_f16(d_tmem, sw128_desc(sa + kk * 32), sw128_desc(sa + 2 * BOX_BYTES + kk * 32), IDESC,
-                      (it > first || kk > 0) ? 1u : 0u);
-          if (issuer) mma_commit(&empty[stage]);
-          if (++stage == SM::N_STAGES) { stage = 0; phase ^= 1; }
+            mma_f16(d_tmem, sw128_desc(a + kk * 32), sw128_desc(b + kk * 32), IDESC, (add || kk > 0) ? 1u : 0u);
+        };
+        for (int first = it; it < end && ok; ++it) {
+          int s0 = stage, s1 = stage;
+          for (int q = 0; q < p.planes; ++q) {   // as in the pair kernel
+            if (!mbar_wait_warp(&full[stage], phase, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            if (q == 1) s1 = stage;
+            if (issuer) {
+              if (q == 0) {
+                product(s0, s0, it > first);
+              } else if (q == 1) {
+                product(s0, s1, true);
+                product(s1, s0, true);
+                product(s1, s1, true);
+                mma_commit(&empty[s1]);
+              } else {
+                product(s0, stage, true);
+                product(stage, s0, true);
+                mma_commit(&empty[stage]);
+              }
+              if (q == p.planes - 1) mma_commit(&empty[s0]);
+            }
+            if (++stage == SM::N_STAGES) { stage = 0; phase ^= 1; }
+          }
         }
         if (!ok) break;
         if (issuer) mma_commit(&tfull[buf]);
@@ -848,7 +868,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       float acc[NT];
 #pragma unroll
       for (int i = 0; i < NT; ++i) acc[i] = 0.f;
-      for (int it = 0; it < iters; it += p.chunk) {
+      for (int it = 0; it < kblocks; it += p.chunk) {
         const bool got = mbar_wait(&tfull[buf], acc_phase, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
           if (lane == 0) atomicOr(err, 4u);
@@ -1529,7 +1549,7 @@ cudaError_t launch_f32_few(const LossParams& p, const void* hidden, const void* 
 
 // k-blocks per accumulator of few rows' logits: short ones cost nothing there
 // (K = 128 or 256).
-int few_chunk(int n) { return n <= 16 ? 2 : 4; }
+int few_chunk(int n, int planes) { return planes == 3 ? F32_CHUNK : (n <= 16 ? 2 : 4); }
 
 // The head as the few-rows kernel reads it: boxes of 32 entries.
 cudaError_t few_head_map(CUtensorMap* map, const void* head, int v, int d, int pitch, int planes) {
@@ -1642,7 +1662,7 @@ static armt_status token_loss(armt_dtype dtype, int n, int vocab, int d, const v
     p.id_bytes = jp.id_bytes = target_bytes;
     p.block_err = (unsigned*)(ws + L.block_err);
     jp.block_err = p.block_err;
-    p.chunk = few_chunk(n);
+    p.chunk = few_chunk(n, L.planes);
     cudaError_t e;
     if (simt) {
       jp.blocks = 148;
@@ -1680,7 +1700,7 @@ static armt_status token_loss(armt_dtype dtype, int n, int vocab, int d, const v
     p.n_valid = jp.n_valid = rp.n_valid;
     p.target = rp.target;
     jp.perm = rp.perm;
-    p.chunk = few ? few_chunk(n) : (f32 ? F32_CHUNK : LSE_CHUNK);
+    p.chunk = few ? few_chunk(n, L.planes) : (f32 ? F32_CHUNK : LSE_CHUNK);
     if (few) e = nr <= 16 ? launch_few<LSE, 16>(maps, p, st) : launch_few<LSE, 64>(maps, p, st);
     else e = launch_products<LSE>(maps, p, (long long)div_up(nr, TILE) * div_up(vocab, TILE), st);
     if (e == cudaSuccess) e = join(nr, r0);

@@ -222,10 +222,10 @@ def loss_reference(hidden, head, targets, scale):
 def logit_error(A, d, planes):
     """A logit's error: a chunk of at most 32 instructions (K = 512), each truncated (2 u) once
     in the instruction's own sum and once in the accumulator, chunks (of 128 at least) added
-    to nearest; fp32 operands: six products, and three terms of 24 bits less what the dropped
-    products hold.  Plain multiply-adds (d / 128 a lane, 5 sums) stay below that."""
-    terms = 6 if planes == 3 else 1
-    chunks = math.ceil(terms * math.ceil(d / 64) / 2)
+    to nearest; fp32 operands: chunks of a k-block's six products (24 instructions), and three
+    terms of 24 bits less what the dropped products hold.  Plain multiply-adds (d / 128 a lane,
+    5 sums) stay below that."""
+    chunks = math.ceil(d / 64) / (1 if planes == 3 else 2)
     return A * ((64 * 2 + chunks) * U + (8 * U if planes == 3 else 0))
 
 
@@ -275,10 +275,11 @@ def check_loss(hidden, head, t, w, scale, got):
     # an exponential below 2^-126, the smallest normal fp32 number, is flushed to zero: exp(l - lse)
     # is then off by up to 2^-126 itself, P by that times its weight
     ep = ep + g.abs() * 2.0 ** -126
-    # products: fp32 operands in chunks of 16 instructions, bf16 over the whole contraction
+    # products: fp32 operands in chunks of 24 instructions (2 u twice each), added to nearest, and
+    # their splits; bf16 over the whole contraction
     def chain(k):
         if planes == 3:
-            return (64 + math.ceil(6 * math.ceil(k / 64) / 4) + 16) * U
+            return (96 + math.ceil(k / 64) + 16) * U
         return (k / 16 + 2) * 4 * U
     want = Q @ W * scale
     mag = (Q.abs() @ W.abs()) * abs(scale)
