@@ -28,9 +28,10 @@
 // over the whole contraction.
 //
 // fp32 operands: x = hi + mid + lo with three bf16 terms (24 bits).  A k-block
-// is three stages, one for each term of both operands, and six products into
-// the same sums: every pair of terms but the three whose product is below
-// 2^-24 of the result.  (Six copies of two tiles instead took 437 ns a product
+// is three stages, one for each term of both operands (lo first), and six
+// products into one accumulator: every pair of terms but the three whose
+// product is below 2^-24 of the result, the small ones first, so that only the
+// last product truncates a sum of full size.  (Six copies of two tiles instead took 437 ns a product
 // of a 256 x 256 tile, against 270 for the product itself.)
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -480,7 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const CUtensorMap* ma = &maps.a;
       const CUtensorMap* mb = ROLE == GRAD && j.dw ? &maps.c : &maps.b;
       const int am = j.m0 + (int)rank * 128, bn = j.n0 + (int)rank * (j.n / 2);
-      for (int kb = 0, q = 0; kb < j.kblocks;) {   // q: the term of both operands
+      for (int kb = 0, q = p.planes - 1; kb < j.kblocks;) {   // q: the term of both operands
         if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
         armed &= ~(1u << stage);
         uint8_t* sa = smem + stage * STAGE_BYTES;
@@ -503,7 +504,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         }
         armed |= 1u << stage;
         if (++stage == STAGES) { stage = 0; phase ^= 1; }
-        if (++q == p.planes) { q = 0; ++kb; }
+        if (--q < 0) { q = p.planes - 1; ++kb; }
       }
     }
     if (!ok) {
@@ -544,25 +545,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                            (add || kk > 0) ? 1u : 0u);
           };
           for (int first = it; it < end && ok; ++it) {
-            int s0 = stage, s1 = stage;   // stages of the first two terms
-            for (int q = 0; q < p.planes; ++q) {
+            int lo = stage, mid = stage;   // stages of the terms; the last one is hi's, or the only one
+            for (int q = p.planes - 1; q >= 0; --q) {
               if (!mbar_wait_cluster_warp(&full[stage], phase, abort_flag)) { ok = false; break; }
-              tc_fence_after();
-              if (q == 1) s1 = stage;
-              if (issuer) {
-                if (q == 0) {
-                  product(s0, s0, it > first);
-                } else if (q == 1) {
-                  product(s0, s1, true);
-                  product(s1, s0, true);
-                  product(s1, s1, true);
-                  mma_commit_pair(&empty[s1], 0x3);
-                } else {
-                  product(s0, stage, true);
-                  product(stage, s0, true);
+              if (q == 1) mid = stage;
+              if (q == 0) {
+                tc_fence_after();
+                if (issuer) {
+                  if (p.planes == 3) {
+                    product(stage, lo, it > first);
+                    product(lo, stage, true);
+                    mma_commit_pair(&empty[lo], 0x3);
+                    product(mid, mid, true);
+                    product(stage, mid, true);
+                    product(mid, stage, true);
+                    mma_commit_pair(&empty[mid], 0x3);
+                  }
+                  product(stage, stage, p.planes == 3 || it > first);
                   mma_commit_pair(&empty[stage], 0x3);
                 }
-                if (q == p.planes - 1) mma_commit_pair(&empty[s0], 0x3);
               }
               if (++stage == STAGES) { stage = 0; phase ^= 1; }
             }
@@ -766,7 +767,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     bool ok = true;
     for (int t = v0; t < v1 && ok; t += 128) {
       const int v = p.v0 + t, boxes = (min(v1 - t, 128) + 31) / 32;
-      for (int kb = 0, q = 0; kb < kblocks;) {
+      for (int kb = 0, q = p.planes - 1; kb < kblocks;) {
         if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
         armed &= ~(1u << stage);
         uint8_t* sa = smem + stage * SM::STAGE;
@@ -778,7 +779,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         }
         armed |= 1u << stage;
         if (++stage == SM::N_STAGES) { stage = 0; phase ^= 1; }
-        if (++q == p.planes) { q = 0; ++kb; }
+        if (--q < 0) { q = p.planes - 1; ++kb; }
       }
     }
     if (!ok) {
@@ -813,25 +814,25 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             mma_f16(d_tmem, sw128_desc(a + kk * 32), sw128_desc(b + kk * 32), IDESC, (add || kk > 0) ? 1u : 0u);
         };
         for (int first = it; it < end && ok; ++it) {
-          int s0 = stage, s1 = stage;
-          for (int q = 0; q < p.planes; ++q) {   // as in the pair kernel
+          int lo = stage, mid = stage;   // as in the pair kernel
+          for (int q = p.planes - 1; q >= 0; --q) {
             if (!mbar_wait_warp(&full[stage], phase, abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            if (q == 1) s1 = stage;
-            if (issuer) {
-              if (q == 0) {
-                product(s0, s0, it > first);
-              } else if (q == 1) {
-                product(s0, s1, true);
-                product(s1, s0, true);
-                product(s1, s1, true);
-                mma_commit(&empty[s1]);
-              } else {
-                product(s0, stage, true);
-                product(stage, s0, true);
+            if (q == 1) mid = stage;
+            if (q == 0) {
+              tc_fence_after();
+              if (issuer) {
+                if (p.planes == 3) {
+                  product(stage, lo, it > first);
+                  product(lo, stage, true);
+                  mma_commit(&empty[lo]);
+                  product(mid, mid, true);
+                  product(stage, mid, true);
+                  product(mid, stage, true);
+                  mma_commit(&empty[mid]);
+                }
+                product(stage, stage, p.planes == 3 || it > first);
                 mma_commit(&empty[stage]);
               }
-              if (q == p.planes - 1) mma_commit(&empty[s0]);
             }
             if (++stage == SM::N_STAGES) { stage = 0; phase ^= 1; }
           }
