@@ -401,7 +401,7 @@ armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d, const voi
 /* Gradients of sum_i d_loss[i] * loss[i] (d_loss [n] fp32) to hidden and head
  * ([type]; either may be null), from the lse of armt_token_loss with the same
  * inputs.  The logits are computed again, one piece of the vocabulary at a
- * time; softmax minus one-hot, divided by the largest |d_loss|, enters the
+ * time; softmax minus one-hot, divided by the largest finite |d_loss|, enters the
  * products as bf16 (as three bf16 terms, 24 bits, for fp32).  Rows without a
  * target have a zero gradient and add nothing to the head's, whatever they
  * hold (d_loss and lse of such rows are not read). */

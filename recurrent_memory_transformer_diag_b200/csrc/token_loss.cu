@@ -973,6 +973,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 // meets four head values; the 4 x NT sums are spread over the lanes while they
 // are added up across the warp, and each lane keeps (max, sum) of one row.
 constexpr int F32_FEW_ROWS = 16;
+constexpr int F32_FEW_SMEM = 200 * 1024;
 constexpr int F32_FEW_THREADS = 384;   // 168 registers: the sums stay in them
 
 // Sum over the lanes of N values each; lane l ends with values l, l + 32, ...
@@ -1100,7 +1101,9 @@ __device__ __forceinline__ void split3(float x, bf16& hi, bf16& mid, bf16& lo) {
   if (!isfinite(x)) mid = lo = __float2bfloat16_rn(0.f);   // inf - inf would be NaN
 }
 
-__device__ __forceinline__ float max_or_nan(float a, float b) { return (b > a || b != b) ? b : a; }   // keeps a NaN of b
+// The larger one; infinities and NaN do not count (the weight of one row must
+// not scale the others').
+__device__ __forceinline__ float max_finite(float a, float b) { return b > a && b < INFINITY ? b : a; }
 
 // counts[k]: rows with a target among 1024 k .. 1024 k + 1023, and their largest
 // |weight|.  Without it every block of order_rows looks through all rows, which
@@ -1113,11 +1116,11 @@ __global__ void __launch_bounds__(COUNT_ROWS) count_rows_kernel(const RowParams 
   float gm = ok && p.d_loss ? fabsf(p.d_loss[i]) : 0.f;
   const int count = __syncthreads_count(ok);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) gm = max_or_nan(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+  for (int o = 16; o; o >>= 1) gm = max_finite(gm, __shfl_xor_sync(0xffffffffu, gm, o));
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = gm;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < 32; ++w) gm = max_or_nan(gm, s_max[w]);
+    for (int w = 1; w < 32; ++w) gm = max_finite(gm, s_max[w]);
     counts[blockIdx.x] = make_int2(count, __float_as_int(gm));
   }
 }
@@ -1138,7 +1141,7 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
     for (int k = threadIdx.x; k < (p.n + COUNT_ROWS - 1) / COUNT_ROWS; k += 256) {
       const int2 c = p.counts[k];
       if (k < here) before += c.x;
-      gm = max_or_nan(gm, __int_as_float(c.y));
+      gm = max_finite(gm, __int_as_float(c.y));
     }
     for (int i = here * COUNT_ROWS + threadIdx.x; i < r0; i += 256) before += valid(i);
   } else {
@@ -1155,14 +1158,14 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         before += ok[u] && i0 + u * 256 < r0;
-        if (ok[u]) gm = max_or_nan(gm, g[u]);
+        if (ok[u]) gm = max_finite(gm, g[u]);
       }
     }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     before += __shfl_xor_sync(0xffffffffu, before, o);
-    gm = max_or_nan(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+    gm = max_finite(gm, __shfl_xor_sync(0xffffffffu, gm, o));
   }
   if (lane == 0) { s_count[warp] = before; s_max[warp] = gm; }
   __syncthreads();
@@ -1170,7 +1173,7 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
   gm = 0.f;
   for (int w = 0; w < 8; ++w) {
     before += s_count[w];
-    gm = max_or_nan(gm, s_max[w]);
+    gm = max_finite(gm, s_max[w]);
   }
   if (threadIdx.x == 0 && blockIdx.x == 0) {
     if (p.clear_err) *p.err = 0;
@@ -1193,7 +1196,7 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const RowParams p) {
         p.perm[at] = i;
         p.target[at] = ok ? (int)load_id(p.targets, p.target_bytes, i) : -1;
         if (p.d_loss) {
-          p.g[at] = ok && gm != 0.f ? p.d_loss[i] / gm : 0.f;
+          p.g[at] = !ok ? 0.f : (gm != 0.f ? p.d_loss[i] / gm : p.d_loss[i] * 0.f);
           p.lse[at] = ok ? p.lse_in[i] : 0.f;
         }
         if (p.loss_out && !ok) {
@@ -1406,7 +1409,7 @@ int few_blocks(int v) { return div_up(v, few_range(v)); }
 // fit the shared memory, up to 3200 columns for 16 of them).
 int f32_few_rows(int n) { return n <= 4 ? 4 : F32_FEW_ROWS; }
 bool f32_few(bool f32, int n, int d, bool grad) {
-  return f32 && !grad && n <= F32_FEW_ROWS && (size_t)f32_few_rows(n) * d * 4 <= 200 * 1024;
+  return f32 && !grad && n <= F32_FEW_ROWS && (size_t)f32_few_rows(n) * d * 4 <= F32_FEW_SMEM;
 }
 
 // Columns of the few-rows kernel's products.
@@ -1542,7 +1545,9 @@ cudaError_t launch_few(const LossMaps& maps, const LossParams& p, cudaStream_t s
 template <int NT>
 cudaError_t launch_f32_few(const LossParams& p, const void* hidden, const void* head, cudaStream_t st) {
   const int smem = NT * p.d * 4;
-  cudaError_t e = cudaFuncSetAttribute(token_loss_f32_few_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // always the most: other threads may launch other sizes between this and the launch
+  cudaError_t e = cudaFuncSetAttribute(token_loss_f32_few_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       F32_FEW_SMEM);
   if (e != cudaSuccess) return e;
   token_loss_f32_few_kernel<NT><<<148, F32_FEW_THREADS, smem, st>>>(p, (const float*)hidden, (const float*)head);
   return cudaGetLastError();

@@ -404,6 +404,23 @@ def test_token_loss_weight_range():
     check_loss(hidden, head, t, one, 1.0, run_loss(hidden, head, t, one))
 
 
+@pytest.mark.parametrize("n", [30, 200])
+def test_token_loss_bad_weights(n):
+    """An infinite and a NaN weight show in their rows' gradients; the other rows' stay."""
+    hidden, head, t, w = loss_inputs(14, n, 500, 64, FP, ignored=0.0)
+    clean = run_loss(hidden, head, t, w)
+    bad = w.clone()
+    bad[3], bad[9] = float("inf"), float("nan")
+    dh = run_loss(hidden, head, t, bad)[2]
+    rest = torch.ones(n, dtype=torch.bool, device="cuda")
+    rest[3] = rest[9] = False
+    assert not torch.isfinite(dh[~rest]).any()
+    # the largest finite weight, which P is divided by, is the same or leaves the same to 2 u a term
+    assert torch.allclose(dh[rest], clean[2][rest], rtol=1e-5, atol=1e-9)
+    only = torch.full_like(w, float("nan"))
+    assert torch.isnan(run_loss(hidden, head, t, only)[2]).all()
+
+
 @pytest.mark.parametrize("which", ["hidden", "head"])
 def test_token_loss_one_gradient(which):
     from recurrent_memory_transformer_diag_b200 import token_loss_grad
@@ -524,6 +541,84 @@ def test_two_graphs_with_their_own_workspaces_replayed_side_by_side():
     torch.cuda.synchronize()
     for a, b in zip(outs, want):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_calls_of_several_threads():
+    """Calls of other sizes from other host threads, each on its own stream."""
+    import threading
+    cases = [loss_inputs(50 + k, n, v, d, dt) for k, (n, v, d, dt) in enumerate(
+        [(3, 900, 2048, FP), (9, 700, 64, FP), (300, 1000, 128, BF), (40, 3000, 256, BF)])]
+    want = [run_loss(*c) for c in cases]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(c, expect):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got = run_loss(*c)
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, expect)):
+                    wrong.append(c[0].shape)
+    threads = [threading.Thread(target=work, args=a) for a in zip(cases, want)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong
+
+
+def test_offsets_past_32_bits():
+    """Tables, hidden states and gradients of more than 2^31 elements."""
+    from recurrent_memory_transformer_diag_b200 import embed, embed_grad, rms_norm, token_loss, token_loss_grad
+    v, d = 300000, 8192
+    g = gen(60)
+    table = torch.zeros(v, d, dtype=BF, device="cuda")
+    ids = torch.tensor([v - 1, 3, v - 2, 262144, 262145, -1, v], device="cuda")
+    ok = ids[:5]
+    table[ok] = randn(g, 5, d).to(BF)
+    out = torch.empty(7, d, dtype=BF, device="cuda")
+    embed(ids, table, out)
+    assert torch.equal(out[:5], table[ok]) and (out[5:] == 0).all()
+    n = 200                                       # sorted ids, and a table zeroed past 2^31 elements
+    many = torch.cat([ok, torch.full((n - 5,), v - 1, device="cuda")])
+    d_out = torch.ones(n, d, dtype=BF, device="cuda")
+    grad = torch.full((v, d), 7.0, dtype=BF, device="cuda")
+    embed_grad(many, d_out, grad)
+    assert (grad[v - 1] == 196).all() and (grad[ok[1:]] == 1).all()
+    grad[ok] = 0
+    assert not grad.any()
+    # a head of that size: the zero rows' logits are 0
+    hidden = (randn(g, 70, d) / 32).to(BF)
+    for rows in (3, 70):
+        t = ok[torch.arange(rows, device="cuda") % 5].clone()
+        h = hidden[:rows].contiguous()
+        loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        token_loss(h, table, t, loss, lse)
+        L = h.double() @ table[ok].double().t()
+        want = torch.log(torch.exp(L).sum(1) + (v - 5))
+        A = (h.double().abs() @ table[ok].double().abs().t()).max(1).values
+        check(lse, want, logit_error(A, d, 1) + 1e-6 * want)
+        w = torch.ones(rows, device="cuda")
+        dh = torch.empty_like(h)
+        grad.fill_(3.0)
+        token_loss_grad(h, table, t, lse, w, dh, grad)
+        P = torch.exp(L - want[:, None])
+        P[torch.arange(rows, device="cuda"), torch.arange(rows, device="cuda") % 5] -= 1
+        dw = P.t() @ h.double()
+        mag = P.abs().t() @ h.double().abs()
+        check(grad[ok], dw, mag * (half(BF) + 1e-4) + dw.abs() * half(BF))
+        p0 = torch.exp(-want)[:, None] * h.double()   # any row of zeros
+        for row in (0, 150000, 262143, 262146, v - 3):
+            check(grad[row], p0.sum(0), p0.abs().sum(0) * (half(BF) + 1e-3) + p0.sum(0).abs() * half(BF))
+        check(dh, P @ table[ok].double(), P.abs() @ table[ok].double().abs() * (half(BF) + 1e-4) + 1e-2 * half(BF)
+              + (P @ table[ok].double()).abs() * half(BF))
+    del grad
+    y = torch.empty_like(table)
+    gain = torch.ones(d, dtype=BF, device="cuda")
+    rms_norm(table, gain, y, None, 1e-6)
+    x = table[ok].double()
+    want = x / (x.square().mean(1, keepdim=True) + 1e-6).sqrt()
+    check(y[ok], want, want.abs() * (half(BF) + 1e-5))
 
 
 def test_given_workspace_and_status():
