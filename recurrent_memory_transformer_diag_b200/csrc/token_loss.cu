@@ -110,6 +110,44 @@ struct LossMaps {
   CUtensorMap out0, out1;     // PROB: P; GRAD: dW, dH partial sums
 };
 
+// Bounded waits (as in the header) that sleep in the hardware: a waiting warp is
+// woken by the barrier or after the hint, instead of reading the clock all the
+// while (the tensor cores are under the power cap here).
+constexpr uint32_t SLEEP_NS = 20000;
+
+template <bool CLUSTER>
+__device__ __forceinline__ bool try_wait_sleeping(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(SLEEP_NS)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(SLEEP_NS)
+        : "memory");
+  return ok != 0;
+}
+
+// By a whole converged warp; the same answer in all lanes.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (__any_sync(0xffffffffu, try_wait_sleeping<CLUSTER>(bar, parity))) return true;
+  const unsigned long long t0 = global_ns();
+  while (true) {
+    if (__any_sync(0xffffffffu, try_wait_sleeping<CLUSTER>(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort_flag != 0 || global_ns() - t0 > WAIT_LIMIT_NS)) return false;
+  }
+}
+
 // One tile of work: D[256 x 256] = A B^T over k-blocks kb = 0 .. kblocks-1.
 struct Job {
   int m0, n0;        // first row / column in the operands' own coordinates
@@ -482,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const CUtensorMap* mb = ROLE == GRAD && j.dw ? &maps.c : &maps.b;
       const int am = j.m0 + (int)rank * 128, bn = j.n0 + (int)rank * (j.n / 2);
       for (int kb = 0, q = p.planes - 1; kb < j.kblocks;) {   // q: the term of both operands
-        if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+        if (!wait_warp<true>(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
         armed &= ~(1u << stage);
         uint8_t* sa = smem + stage * STAGE_BYTES;
         if (issuer && !p.debug_no_loads) {
@@ -533,7 +571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         const uint32_t idesc = idesc_f16(j.n, 1, TILE) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
         const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
         for (int it = 0; it < j.kblocks && ok;) {
-          if (!mbar_wait_cluster_warp(&tempty[buf], acc_phase ^ 1, abort_flag)) { ok = false; break; }
+          if (!wait_warp<true>(&tempty[buf], acc_phase ^ 1, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + (uint32_t)(buf * TILE);
           const int end = min(j.kblocks, it + p.chunk);
@@ -547,7 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           for (int first = it; it < end && ok; ++it) {
             int lo = stage, mid = stage;   // stages of the terms; the last one is hi's, or the only one
             for (int q = p.planes - 1; q >= 0; --q) {
-              if (!mbar_wait_cluster_warp(&full[stage], phase, abort_flag)) { ok = false; break; }
+              if (!wait_warp<true>(&full[stage], phase, abort_flag)) { ok = false; break; }
               if (q == 1) mid = stage;
               if (q == 0) {
                 tc_fence_after();
@@ -604,8 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
       }
       for (int it = 0; it < j.kblocks; it += p.chunk) {
-        const bool got = mbar_wait_cluster(&tfull[buf], acc_phase, abort_flag);
-        if (!__all_sync(0xffffffffu, got)) {
+        if (!wait_warp<true>(&tfull[buf], acc_phase, abort_flag)) {
           if (lane == 0) atomicOr(p.err, 4u);
           *abort_flag = 1;
           ok = false;
@@ -768,7 +805,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     for (int t = v0; t < v1 && ok; t += 128) {
       const int v = p.v0 + t, boxes = (min(v1 - t, 128) + 31) / 32;
       for (int kb = 0, q = p.planes - 1; kb < kblocks;) {
-        if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+        if (!wait_warp<false>(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
         armed &= ~(1u << stage);
         uint8_t* sa = smem + stage * SM::STAGE;
         if (issuer && !p.debug_no_loads) {
@@ -803,7 +840,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     bool ok = true;
     for (int t = v0; t < v1 && ok; t += 128) {
       for (int it = 0; it < kblocks && ok;) {
-        if (!mbar_wait_warp(&tempty[buf], acc_phase ^ 1, abort_flag)) { ok = false; break; }
+        if (!wait_warp<false>(&tempty[buf], acc_phase ^ 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(buf * NT);
         const int end = min(kblocks, it + p.chunk);
@@ -816,7 +853,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         for (int first = it; it < end && ok; ++it) {
           int lo = stage, mid = stage;   // as in the pair kernel
           for (int q = p.planes - 1; q >= 0; --q) {
-            if (!mbar_wait_warp(&full[stage], phase, abort_flag)) { ok = false; break; }
+            if (!wait_warp<false>(&full[stage], phase, abort_flag)) { ok = false; break; }
             if (q == 1) mid = stage;
             if (q == 0) {
               tc_fence_after();
@@ -870,8 +907,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 #pragma unroll
       for (int i = 0; i < NT; ++i) acc[i] = 0.f;
       for (int it = 0; it < kblocks; it += p.chunk) {
-        const bool got = mbar_wait(&tfull[buf], acc_phase, abort_flag);
-        if (!__all_sync(0xffffffffu, got)) {
+        if (!wait_warp<false>(&tfull[buf], acc_phase, abort_flag)) {
           if (lane == 0) atomicOr(err, 4u);
           *abort_flag = 1;
           ok = false;
