@@ -88,6 +88,7 @@ struct LossParams {
   int chunk;                  // k-blocks per accumulator
   float scale;
   const int* n_valid;         // rows with a target (device)
+  const int* perm;            // fp32 few rows, PROB: where an ordered row stands in hidden
   const int* target;          // per row in order
   // LSE
   float2* part; int part_pitch; float* target_logit;
@@ -503,7 +504,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
 
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CTRL_REGS));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CTRL_REGS));
   if (skip) {
     // nothing to do
   } else if (warp == 0) {
@@ -731,7 +732,10 @@ struct Few {
   static constexpr int ROWS = N_STAGES * STAGE;           // lse, g, target of the rows
   static constexpr int BARS = ROWS + 3 * NT * 4;
   static constexpr int TOTAL = BARS + 512 + 1024;
-  static constexpr int COLS = 2 * NT < 32 ? 32 : 2 * NT;  // TMEM columns: two accumulators
+  // accumulators: a chunk is one or two k-blocks (0.4 us of the head each), shorter
+  // than the way from the products to the epilogue and back
+  static constexpr int BUFS = NT == 16 ? 8 : 4;
+  static constexpr int COLS = BUFS * NT;   // TMEM columns
   static_assert(TOTAL <= 227 * 1024, "shared memory per CTA");
 };
 constexpr int FEW_THREADS = 256;     // warp 0 copies, warp 1 products, warps 4..7 epilogue
@@ -749,8 +753,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::BARS);
   uint64_t* empty = full + SM::N_STAGES;
   uint64_t* tfull = empty + SM::N_STAGES;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
+  uint64_t* tempty = tfull + SM::BUFS;
+  uint64_t* drain = tempty + SM::BUFS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ unsigned skip_cta;
@@ -767,7 +771,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < SM::BUFS; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 4);
     }
@@ -876,7 +880,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         }
         if (!ok) break;
         if (issuer) mma_commit(&tfull[buf]);
-        if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+        if (++buf == SM::BUFS) { buf = 0; acc_phase ^= 1; }
       }
     }
     if (!ok) {
@@ -925,7 +929,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tempty[buf]);
-        if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+        if (++buf == SM::BUFS) { buf = 0; acc_phase ^= 1; }
       }
       if (!ok) break;
       const bool in = v < v1;
@@ -1002,12 +1006,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-// The loss of up to 16 fp32 rows: bound by reading the fp32 head once, which
+// LSE and PROB of up to 16 fp32 rows: bound by reading the fp32 head once, which
 // splitting it into bf16 terms would not allow (13 rows, 43440 x 1704: 292 us
 // that way).  Plain fp32 multiply-adds: the hidden rows in shared memory, a
 // warp four vocabulary entries at a time so that every value read from there
 // meets four head values; the 4 x NT sums are spread over the lanes while they
-// are added up across the warp, and each lane keeps (max, sum) of one row.
+// are added up across the warp, and each lane keeps (max, sum) of one row.  The
+// gradient's logits come from here too: they have to be the very numbers that
+// the lse was made of, or the difference (1e-6 of a logit of 14) shows in P.
 constexpr int F32_FEW_ROWS = 16;
 constexpr int F32_FEW_SMEM = 200 * 1024;
 constexpr int F32_FEW_THREADS = 384;   // 168 registers: the sums stay in them
@@ -1033,7 +1039,7 @@ __device__ __forceinline__ void spread_sum(float* v, int lane) {
   }
 }
 
-template <int NT>
+template <int ROLE, int NT>
 __global__ void __launch_bounds__(F32_FEW_THREADS, 1) token_loss_f32_few_kernel(const LossParams p, const float* hidden,
                                                                                const float* head) {
   extern __shared__ __align__(16) float s_h[];   // [NT][d]
@@ -1041,23 +1047,26 @@ __global__ void __launch_bounds__(F32_FEW_THREADS, 1) token_loss_f32_few_kernel(
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d = p.d;
   for (int k = threadIdx.x * 4; k < NT * d; k += F32_FEW_THREADS * 4) {
-    const int r = k / d;
+    const int r = k / d, c = k - r * d;
     // a row without a target counts for nothing, whatever it holds
-    const bool ok = r < p.n_rows && target_of(p.ids, p.id_bytes, r, p.vocab) >= 0;
+    const bool ok = ROLE == LSE ? r < p.n_rows && target_of(p.ids, p.id_bytes, r, p.vocab) >= 0 : r < *p.n_valid;
     *reinterpret_cast<float4*>(s_h + k) =
-        ok ? *reinterpret_cast<const float4*>(hidden + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        ok ? *reinterpret_cast<const float4*>(hidden + (long long)(ROLE == LSE ? r : p.perm[r]) * d + c)
+           : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   __syncthreads();
   // value i = 32 u + lane of the sums: entry i / NT, row i % NT
   constexpr int U = N / 32 > 0 ? N / 32 : 1;
   const int row = lane % NT;
-  const int target = row < p.n_rows ? target_of(p.ids, p.id_bytes, row, p.vocab) : -1;
+  const int target = row >= p.n_rows ? -1 : (ROLE == LSE ? target_of(p.ids, p.id_bytes, row, p.vocab) : p.target[row]);
+  const float weight = ROLE == PROB && row < p.n_rows ? p.g[row] : 0.f, lse = ROLE == PROB && row < p.n_rows ? p.lse[row] : 0.f;
   float m = -INFINITY, sum = 0.f;
-  const int groups = (p.vocab + 3) / 4;
+  const int groups = (p.vc + 3) / 4;
+  const float* piece = head + (long long)p.v0 * d;
   for (int g = blockIdx.x * (F32_FEW_THREADS / 32) + warp; g < groups; g += gridDim.x * (F32_FEW_THREADS / 32)) {
     const float* w[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = head + (long long)min(4 * g + e, p.vocab - 1) * d;
+    for (int e = 0; e < 4; ++e) w[e] = piece + (long long)min(4 * g + e, p.vc - 1) * d;
     float2 acc[4][NT];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -1091,13 +1100,26 @@ __global__ void __launch_bounds__(F32_FEW_THREADS, 1) token_loss_f32_few_kernel(
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = 32 * u + lane, entry = 4 * g + i / NT;
-      if (i < N && entry < p.vocab) {
+      if (i < N && entry < p.vc) {
         const float l = v[u] * p.scale;
-        add_logit(l, m, sum);
-        if (entry == target) p.target_logit[row] = l;
+        if constexpr (ROLE == LSE) {
+          add_logit(l, m, sum);
+          if (entry == target) p.target_logit[row] = l;
+        } else if (row < p.n_rows) {
+          float x = weight * ex2((l - lse) * LOG2E);
+          if (p.v0 + entry == target) x -= weight;
+          if (weight == 0.f) x = 0.f;
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {   // as the few-rows kernel leaves it: [term][entry][16]
+            const bf16 y = __float2bfloat16_rn(x);
+            p.p_out[((long long)q * p.vc + entry) * 16 + row] = y;
+            x -= __bfloat162float(y);
+          }
+        }
       }
     }
   }
+  if (ROLE != LSE) return;
   // lanes of the same row
 #pragma unroll
   for (int o = 16; o >= NT; o >>= 1) {
@@ -1441,11 +1463,11 @@ int div_up(int a, int b) { return (a + b - 1) / b; }
 
 int few_blocks(int v) { return div_up(v, few_range(v)); }
 
-// Whether the loss of fp32 rows runs on plain multiply-adds (the rows have to
+// Whether the logits of fp32 rows run on plain multiply-adds (the rows have to
 // fit the shared memory, up to 3200 columns for 16 of them).
 int f32_few_rows(int n) { return n <= 4 ? 4 : F32_FEW_ROWS; }
-bool f32_few(bool f32, int n, int d, bool grad) {
-  return f32 && !grad && n <= F32_FEW_ROWS && (size_t)f32_few_rows(n) * d * 4 <= F32_FEW_SMEM;
+bool f32_few(bool f32, int n, int d) {
+  return f32 && n <= F32_FEW_ROWS && (size_t)f32_few_rows(n) * d * 4 <= F32_FEW_SMEM;
 }
 
 // Columns of the few-rows kernel's products.
@@ -1464,7 +1486,7 @@ struct Layout {
     // second terms stand as further rows of P, beside the same hidden rows again
     two_terms = grad && !f32 && n <= FEW_ROWS ? few_cols(n) : 0;
     g_rows = two_terms ? 2 * two_terms : n;
-    const bool simt = f32_few(f32, n, d, grad);
+    const bool simt = f32_few(f32, n, d);
     rows = grad ? n : (n < LOSS_ROWS ? n : LOSS_ROWS);
     n_parts = simt ? 148 * (F32_FEW_THREADS / 32) : (n <= FEW_ROWS ? 4 * few_blocks(v) : 2 * div_up(v, TILE));
     vc = v; pieces = 1; splits = k_split = dw_k = 0; dw_splits = 1;
@@ -1506,7 +1528,7 @@ struct Layout {
     lse = take(grad ? (size_t)rows * 4 : 0);
     tlogit = take(grad ? 0 : (size_t)rows * 4);
     part = take(grad ? 0 : (size_t)n_parts * rows * 8);
-    head = take(f32 && !simt ? (size_t)3 * v * dp * 2 : 0);
+    head = take(f32 && (grad || !simt) ? (size_t)3 * v * dp * 2 : 0);
     p = take(grad ? (size_t)planes * (two_terms ? g_rows : (n <= FEW_ROWS ? few_cols(n) : n)) * round_up(vc, 64) * 2 : 0);
     dh = take(grad ? (size_t)splits * g_rows * dq * 4 : 0);
     dw = take(dw_splits > 1 ? (size_t)dw_splits * vc * dq * 4 : 0);
@@ -1578,20 +1600,23 @@ cudaError_t launch_few(const LossMaps& maps, const LossParams& p, cudaStream_t s
   return cudaGetLastError();
 }
 
-template <int NT>
+template <int ROLE, int NT>
 cudaError_t launch_f32_few(const LossParams& p, const void* hidden, const void* head, cudaStream_t st) {
   const int smem = NT * p.d * 4;
   // always the most: other threads may launch other sizes between this and the launch
-  cudaError_t e = cudaFuncSetAttribute(token_loss_f32_few_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       F32_FEW_SMEM);
+  cudaError_t e = cudaFuncSetAttribute(token_loss_f32_few_kernel<ROLE, NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, F32_FEW_SMEM);
   if (e != cudaSuccess) return e;
-  token_loss_f32_few_kernel<NT><<<148, F32_FEW_THREADS, smem, st>>>(p, (const float*)hidden, (const float*)head);
+  token_loss_f32_few_kernel<ROLE, NT><<<148, F32_FEW_THREADS, smem, st>>>(p, (const float*)hidden, (const float*)head);
   return cudaGetLastError();
 }
 
-// k-blocks per accumulator of few rows' logits: short ones cost nothing there
-// (K = 128 or 256).
-int few_chunk(int n, int planes) { return planes == 3 ? F32_CHUNK : (n <= 16 ? 2 : 4); }
+// k-blocks per accumulator of few rows' logits, K = 64 or 128: the truncation of
+// longer ones show: a row's loss is a small difference of two logits, and of
+// one row nothing averages out (error of the loss of one row against 64 bits,
+// 12 inputs: K = 64 2.4e-7 in 98 us, K = 128 2.8e-7 in 94, K = 256 7.2e-7 in
+// 86; the plain fp32 form 2.0e-7).
+int few_chunk(int n, int planes) { return planes == 3 ? F32_CHUNK : (n <= 16 ? 1 : 2); }
 
 // The head as the few-rows kernel reads it: boxes of 32 entries.
 cudaError_t few_head_map(CUtensorMap* map, const void* head, int v, int d, int pitch, int planes) {
@@ -1697,7 +1722,7 @@ static armt_status token_loss(armt_dtype dtype, int n, int vocab, int d, const v
     return cudaGetLastError();
   };
   LossMaps maps{};
-  const bool simt = f32_few(f32, n, d, false);
+  const bool simt = f32_few(f32, n, d);
   if (simt || (!f32 && n <= FEW_ROWS)) {   // few rows, in their own order: two launches
     p.n_rows = p.part_pitch = n;
     p.ids = jp.ids = targets;
@@ -1708,7 +1733,7 @@ static armt_status token_loss(armt_dtype dtype, int n, int vocab, int d, const v
     cudaError_t e;
     if (simt) {
       jp.blocks = 148;
-      e = n <= 4 ? launch_f32_few<4>(p, hidden, head, st) : launch_f32_few<F32_FEW_ROWS>(p, hidden, head, st);
+      e = n <= 4 ? launch_f32_few<LSE, 4>(p, hidden, head, st) : launch_f32_few<LSE, F32_FEW_ROWS>(p, hidden, head, st);
     } else {
       jp.blocks = few_blocks(vocab);
       e = few_map(&maps.a, hidden, n, d, d, 1);
@@ -1795,7 +1820,7 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
   if (e == cudaSuccess && d_hidden) e = make_map(&mg.out1, ws + L.dh, true, d, L.dq, L.g_rows, L.splits, 32, 32);
   LossParams p{};
   p.n_rows = n; p.d = d; p.vocab = vocab; p.planes = L.planes; p.scale = scale;
-  p.n_valid = rp.n_valid; p.target = rp.target; p.lse = rp.lse; p.g = rp.g; p.g_max = rp.g_max; p.err = rp.err;
+  p.n_valid = rp.n_valid; p.perm = rp.perm; p.target = rp.target; p.lse = rp.lse; p.g = rp.g; p.g_max = rp.g_max; p.err = rp.err;
   p.want_dw = d_head != nullptr; p.want_dh = d_hidden != nullptr; p.dw_bf16 = !f32; p.k_split = L.k_split;
   p.dw_splits = L.dw_splits; p.dw_k = L.dw_k;
   const bool few = n <= FEW_ROWS;
@@ -1818,6 +1843,8 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     p.p_trans = few;
     if (e == cudaSuccess)
       e = !few ? launch_products<PROB>(mp, p, (long long)mt * nt, st)
+          : f32_few(f32, n, d) ? (n <= 4 ? launch_f32_few<PROB, 4>(p, hidden, head, st)
+                                         : launch_f32_few<PROB, F32_FEW_ROWS>(p, hidden, head, st))
                : (n <= 16 ? launch_few<PROB, 16>(mp, p, st) : launch_few<PROB, 64>(mp, p, st));
     LossParams pg = p;
     pg.n_rows = L.g_rows;
