@@ -86,6 +86,7 @@ struct LossParams {
   int v0, vc;                 // vocabulary piece
   int panels;                 // P is kept in panels of 64 columns: [term][panel][row][64], 4 to 8 KB a copy
   int chunk;                  // k-blocks per accumulator
+  int tile_n;                 // LSE, PROB: columns of a tile, 256 or 128
   float scale;
   const int* n_valid;         // rows with a target (device)
   const int* perm;            // fp32 few rows, PROB: where an ordered row stands in hidden
@@ -154,7 +155,7 @@ struct Job {
   int m0, n0;        // first row / column in the operands' own coordinates
   int ka, kb;        // first k coordinate in A / B
   int kblocks;
-  int n;             // columns computed: 256, or 128 where the gradient's width ends there
+  int n;             // columns computed: 256, or 128 (few tiles, or where the gradient's width ends there)
   bool dw;           // GRAD: a tile of dW (A is P transposed)
   int split;         // GRAD, dH: which partial sum
   int ntile;         // LSE: index of the vocabulary tile
@@ -166,7 +167,7 @@ struct Jobs {
   bool dw_first;   // the longer contraction first, so that the shorter tiles fill the end
   __device__ Jobs(const LossParams& p, int nv) {
     mt = (nv + TILE - 1) / TILE;
-    nt = (p.vc + TILE - 1) / TILE;
+    nt = ROLE == GRAD ? (p.vc + TILE - 1) / TILE : (p.vc + p.tile_n - 1) / p.tile_n;
     dt = (p.d + TILE - 1) / TILE;
     if (ROLE == GRAD) {
       n_dw = p.want_dw ? nt * dt * p.dw_splits : 0;
@@ -193,7 +194,8 @@ struct Jobs {
       const int mg = min(ROW_GROUP, mt - grp * ROW_GROUP);
       j.ntile = r / mg;
       j.m0 = (grp * ROW_GROUP + r - j.ntile * mg) * TILE;
-      j.n0 = p.v0 + j.ntile * TILE;
+      j.n = p.tile_n;
+      j.n0 = p.v0 + j.ntile * p.tile_n;
       j.ka = j.kb = 0;
       j.kblocks = (p.d + BK - 1) / BK;
     } else if (dw_first ? t < n_dw : t >= n_dh) {
@@ -336,6 +338,7 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
   const int row = j.m0 + row_in_tile;
   const int wrow0 = row - lane;
   const int col0 = j.n0 + half * 128;
+  if (half * 128 >= j.n) return;   // a tile of 128 columns
   if constexpr (ROLE == LSE) {
     const float2 scale2 = make_float2(p.scale, p.scale);
 #pragma unroll
@@ -364,7 +367,7 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
     }
     s2[0] = __fadd2_rn(s2[0], s2[1]);
     if (row < nv) {
-      p.part[(long long)(2 * j.ntile + half) * p.part_pitch + row] = make_float2(m, s2[0].x + s2[0].y);
+      p.part[(long long)(j.ntile * (j.n / 128) + half) * p.part_pitch + row] = make_float2(m, s2[0].x + s2[0].y);
       const unsigned at = (unsigned)(rd.target - col0);
       if (at < 128u) {
         float t = 0.f;
@@ -1473,6 +1476,10 @@ bool f32_few(bool f32, int n, int d) {
 // Columns of the few-rows kernel's products.
 int few_cols(int n) { return n <= 16 ? 16 : FEW_ROWS; }
 
+// Columns of a tile of logits: 256; 128 where those would leave most of the
+// device idle (the products' time is the tile's, its copies' less than halved).
+int logit_tile(int n, int v) { return div_up(n, TILE) * div_up(v, TILE) * 2 <= 74 ? 128 : 256; }
+
 // Workspace of one call, laid out in order.
 struct Layout {
   int planes, dp, dq, rows, g_rows, two_terms, pieces, vc, splits, k_split, dw_splits, dw_k, n_parts;
@@ -1488,7 +1495,8 @@ struct Layout {
     g_rows = two_terms ? 2 * two_terms : n;
     const bool simt = f32_few(f32, n, d);
     rows = grad ? n : (n < LOSS_ROWS ? n : LOSS_ROWS);
-    n_parts = simt ? 148 * (F32_FEW_THREADS / 32) : (n <= FEW_ROWS ? 4 * few_blocks(v) : 2 * div_up(v, TILE));
+    n_parts = simt ? 148 * (F32_FEW_THREADS / 32)
+                   : (n <= FEW_ROWS ? 4 * few_blocks(v) : logit_tile(rows, v) / 128 * div_up(v, logit_tile(rows, v)));
     vc = v; pieces = 1; splits = k_split = dw_k = 0; dw_splits = 1;
     if (grad) {
       long long w = P_BYTES / ((long long)g_rows * 2 * planes) / TILE * TILE;
@@ -1767,9 +1775,10 @@ static armt_status token_loss(armt_dtype dtype, int n, int vocab, int d, const v
     p.n_valid = jp.n_valid = rp.n_valid;
     p.target = rp.target;
     jp.perm = rp.perm;
+    p.tile_n = logit_tile(L.rows, vocab);   // the same for every pass: the parts are laid out for it
     p.chunk = few ? few_chunk(n, L.planes) : (f32 ? F32_CHUNK : LSE_CHUNK);
     if (few) e = nr <= 16 ? launch_few<LSE, 16>(maps, p, st) : launch_few<LSE, 64>(maps, p, st);
-    else e = launch_products<LSE>(maps, p, (long long)div_up(nr, TILE) * div_up(vocab, TILE), st);
+    else e = launch_products<LSE>(maps, p, (long long)div_up(nr, TILE) * div_up(vocab, p.tile_n), st);
     if (e == cudaSuccess) e = join(nr, r0);
   }
   return cuda_status(e);
@@ -1839,10 +1848,11 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     if (e == cudaSuccess && !few) e = make_map(&mp.out0, ws + L.p, false, 64, 64, n, p.panels * L.planes, 64, 32);
     p.chunk = f32 ? F32_CHUNK : WHOLE_CHUNK;
     const int nt = div_up(p.vc, TILE);
+    p.tile_n = logit_tile(n, p.vc);
     p.p_out = (bf16*)(ws + L.p);
     p.p_trans = few;
     if (e == cudaSuccess)
-      e = !few ? launch_products<PROB>(mp, p, (long long)mt * nt, st)
+      e = !few ? launch_products<PROB>(mp, p, (long long)mt * div_up(p.vc, p.tile_n), st)
           : f32_few(f32, n, d) ? (n <= 4 ? launch_f32_few<PROB, 4>(p, hidden, head, st)
                                          : launch_f32_few<PROB, F32_FEW_ROWS>(p, hidden, head, st))
                : (n <= 16 ? launch_few<PROB, 16>(mp, p, st) : launch_few<PROB, 64>(mp, p, st));
