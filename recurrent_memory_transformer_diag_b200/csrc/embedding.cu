@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(256) embed_kernel(const void* ids, int id_byte
 // ---------------------------------------------------------------- gradient, few tokens
 // Most tokens for the one-launch gradient.  Its time grows with the tokens of
 // one row, which one group of threads adds up: 870 tokens with a few frequent
-// ids (table 1323 x 1168) took 148 us here and 25 us sorted; 67 tokens 6 us.
+// ids (table 1323 x 1168) took 148 us here and 22 us sorted; 128 tokens 7 us.
 constexpr int SCAN_MAX = 128;
 // Table rows of a block: enough blocks for the device where the table is small.
 int scan_rows(int vocab) { return vocab >= 32 * 592 ? 32 : (vocab >= 592 ? vocab / 592 : 1); }
@@ -289,22 +289,26 @@ __global__ void __launch_bounds__(1024, 1) sort_block_kernel(const void* ids, in
   int* s_pos = dyn + BLOCK_SORT_MAX;
   unsigned short* cnt = reinterpret_cast<unsigned short*>(dyn + 2 * BLOCK_SORT_MAX);   // [warp][digit]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per_warp = (n + 1023) / 1024 * 32;   // keys of a warp, consecutive
+  // a warp's keys are consecutive, 256 of them: the fewer warps have any, the
+  // less there is to add up (870 tokens: 14.8 us with 32 warps of 32)
+  constexpr int per_warp = 32 * BLOCK_SORT_STEPS;
+  const int warps = (n + per_warp - 1) / per_warp;
   const int base = warp * per_warp;
   int key[BLOCK_SORT_STEPS], pos[BLOCK_SORT_STEPS];
 #pragma unroll
   for (int s = 0; s < BLOCK_SORT_STEPS; ++s) {
-    const int k = s * 32 + lane, i = base + k;
+    const int i = base + s * 32 + lane;
     pos[s] = i;
-    key[s] = k < per_warp && i < n ? sort_key(ids, id_bytes, nullptr, i, vocab) : -1;
+    key[s] = i < n ? sort_key(ids, id_bytes, nullptr, i, vocab) : -1;
   }
   if (threadIdx.x == 0) *clear = 0;
   for (int shift = 0; shift < 31 && (shift == 0 || (vocab >> shift) != 0); shift += RADIX_BITS) {
-    for (int i = threadIdx.x; i < BLOCK_SORT_WARPS * RADIX / 2; i += 1024) reinterpret_cast<int*>(cnt)[i] = 0;
+    for (int i = threadIdx.x; i < warps * RADIX / 2; i += 1024) reinterpret_cast<int*>(cnt)[i] = 0;
     __syncthreads();
     int rank[BLOCK_SORT_STEPS];
 #pragma unroll
     for (int s = 0; s < BLOCK_SORT_STEPS; ++s) {
+      if (base + s * 32 >= n) break;   // the whole warp
       const bool in = key[s] >= 0;
       const int dg = in ? (key[s] >> shift) & (RADIX - 1) : RADIX;
       const unsigned same = same_digit(dg);
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(1024, 1) sort_block_kernel(const void* ids, in
     int total = 0, incl = 0;   // a thread per digit: exclusive sums over the warps, then over the digits
     if (threadIdx.x < RADIX) {
 #pragma unroll 8
-      for (int w = 0; w < BLOCK_SORT_WARPS; ++w) {
+      for (int w = 0; w < warps; ++w) {
         const int c = cnt[w * RADIX + threadIdx.x];
         cnt[w * RADIX + threadIdx.x] = (unsigned short)total;
         total += c;
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(1024, 1) sort_block_kernel(const void* ids, in
       int start = incl - total;
       for (int w = 0; w < warp; ++w) start += s_scan[w];
 #pragma unroll 8
-      for (int w = 0; w < BLOCK_SORT_WARPS; ++w) cnt[w * RADIX + threadIdx.x] += (unsigned short)start;
+      for (int w = 0; w < warps; ++w) cnt[w * RADIX + threadIdx.x] += (unsigned short)start;
     }
     __syncthreads();
 #pragma unroll
@@ -353,8 +357,8 @@ __global__ void __launch_bounds__(1024, 1) sort_block_kernel(const void* ids, in
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < BLOCK_SORT_STEPS; ++s) {
-      const int k = s * 32 + lane, i = base + k;
-      if (k < per_warp && i < n) {
+      const int i = base + s * 32 + lane;
+      if (i < n) {
         key[s] = s_key[i];
         pos[s] = s_pos[i];
       }
@@ -613,7 +617,8 @@ cudaError_t embed_grad(int n, int vocab, int d, const void* ids, int id_bytes, c
   p.n_open = n_open;
   const int fill = accumulate ? 0 : (vocab + FILL_ROWS - 1) / FILL_ROWS;
   embed_grad_sum_kernel<T><<<p.sum_blocks + fill, 256, 0, st>>>(p, d_out, d_table);
-  embed_grad_join_kernel<T><<<148 * 8, 256, 0, st>>>(p, d_table);
+  const long long pieces = (long long)p.chunks * ((d + 255) / 256);   // at most
+  embed_grad_join_kernel<T><<<(int)(pieces < 148 * 8 ? pieces : 148 * 8), 256, 0, st>>>(p, d_table);
   return cudaGetLastError();
 }
 
