@@ -251,14 +251,23 @@ class Armt:
         ``forward_ex``.  The embeddings, hidden states and workspaces live for the
         call, in PyTorch's allocator, on the call's stream."""
         from . import operators as ops
-        n, d = n_segments * seg_len, self.cfg.d_model
-        for name, t in (("ids", ids), ("targets", targets)):
-            if t.numel() != n:
-                raise ArmtError(1, "Armt.score", f"{name} must hold n_segments * seg_len ids")
-        if table.shape[-1] != d or head.shape[-1] != d:
-            raise ArmtError(1, "Armt.score", "table and head must be as wide as the model")
-        if table.dtype != ops.torch_type(self.cfg.dtype):
-            raise ArmtError(1, "Armt.score", "table, head and gain must have the context's type")
+        w, c = "Armt.score", self.cfg
+        n, d = n_segments * seg_len, c.d_model
+        # everything is looked at before the forward changes A and z
+        _, vocab, _, dev = ops._matrix(w, "table", table)
+        dtype, f32 = ops.torch_type(c.dtype), ops.torch_type("fp32")
+        ops._tensor(w, "table", table, dtype, (vocab, d), dev)
+        ops._matrix(w, "head", head)
+        ops._tensor(w, "head", head, dtype, (head.shape[0], d), dev)
+        if gain is not None:
+            ops._tensor(w, "gain", gain, dtype, (d,), dev)
+        ops._ids(w, "ids", ids, n, dev)
+        ops._ids(w, "targets", targets, n, dev)
+        ops._tensor(w, "loss", loss, f32, (n,), dev)
+        ops._tensor(w, "A", A, f32, (c.n_layers, d, c.phi_dim), dev)
+        ops._tensor(w, "z", z, f32, (c.n_layers, c.phi_dim), dev)
+        ops._apart(w, [("loss", loss), ("A", A), ("z", z)],
+                   [("ids", ids), ("targets", targets), ("table", table), ("head", head), ("gain", gain)])
         with ops.on_stream(stream, table.device):
             x = table.new_empty(n, d)
             ops.embed(ids, table, x, scale=embed_scale)

@@ -638,7 +638,7 @@ def test_given_workspace_and_status():
 def test_score_runs_ids_to_losses(name):
     """Armt.score: the losses of its embedding, forward, norm and loss, against the
     64-bit result from the forward's own hidden states; and streamed in two calls."""
-    from recurrent_memory_transformer_diag_b200 import Armt, CONFIGS, make_weights
+    from recurrent_memory_transformer_diag_b200 import Armt, ArmtError, CONFIGS, make_weights
     cfg = CONFIGS[name]
     dt = BF if cfg.dtype == "bf16" else FP
     S, T, d, v = 4, cfg.seg_len, cfg.d_model, 515
@@ -675,6 +675,17 @@ def test_score_runs_ids_to_losses(name):
             parts.append(p)
         torch.cuda.synchronize()
         assert torch.equal(torch.cat(parts), loss)
+        # a wrong tensor is refused before the state changes
+        good = {"ids": ids, "targets": targets, "table": table, "head": head, "gain": gain, "loss": loss}
+        for name, bad in (("ids", ids[1:]), ("targets", targets.float()), ("table", table[:, :8].contiguous()),
+                          ("head", head.to(FP if dt == BF else BF)), ("gain", gain[1:]), ("loss", loss[1:]),
+                          ("loss", A3.view(-1)[:S * T])):
+            q = {**good, name: bad}
+            before = A3.clone(), z3.clone()
+            with pytest.raises(ArmtError):
+                m.score(q["ids"], q["targets"], S, T, q["table"], q["head"], q["gain"], q["loss"], A3, z3)
+            torch.cuda.synchronize()
+            assert torch.equal(A3, before[0]) and torch.equal(z3, before[1])
 
 
 @pytest.mark.parametrize("rows", [4, 40, 200])
