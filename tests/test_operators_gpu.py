@@ -11,6 +11,18 @@ import torch
 
 pytestmark = pytest.mark.gpu
 
+
+
+@pytest.fixture(scope="module", autouse=True)
+def leave_nothing():
+    """Tensors that closures and caught exceptions still hold in cycles are freed here,
+    not at some later moment in a test that watches the allocator."""
+    yield
+    import gc
+    gc.collect()
+    torch.cuda.empty_cache()
+
+
 BF, FP = torch.bfloat16, torch.float32
 U = 2.0 ** -24
 
