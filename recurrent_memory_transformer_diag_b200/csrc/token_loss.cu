@@ -402,6 +402,14 @@ __device__ __forceinline__ void finish_tile(const LossParams& p, const LossMaps&
 #pragma unroll
       for (int i = 0; i < 64; ++i) sums[i] = make_float2(0.f, 0.f);
     }
+    if (col0 + 128 > p.vocab) {   // the last tile: columns past the vocabulary (logits of 0) may be infinite, and dH
+                                  // contracts over the whole panel that they stand in
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        if (col0 + 2 * i >= p.vocab) sums[i].x = 0.f;
+        if (col0 + 2 * i + 1 >= p.vocab) sums[i].y = 0.f;
+      }
+    }
     const int pc = col0 - p.v0;   // column in the piece
     if (wrow0 >= p.n_rows || pc >= p.vc) return;   // nothing of these panels is in P
     for (int t = 0; t + 1 < p.planes; ++t) {

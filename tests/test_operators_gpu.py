@@ -781,3 +781,28 @@ def test_wrappers_refuse_workspaces():
     with pytest.raises(ArmtError):   # results inside the workspace
         ws = torch.empty(size + v * d * 2, dtype=torch.uint8, device="cuda")
         embed_grad(t, hidden, ws[:v * d * 2].view(BF).view(v, d), workspace=ws)
+
+
+# ------------------------------------------------------------------ logits far below zero
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("at", [-100.0, -200.0])
+@pytest.mark.parametrize("n,v,d", [(40, 300, 64), (65, 300, 64), (65, 1025, 64), (300, 300, 136), (300, 1025, 64),
+                                   (3000, 1000, 64)])
+def test_token_loss_logits_far_below_zero(n, v, d, at, dtype):
+    """Every logit near `at`, so that exp(0 - lse) is past fp32: columns behind a vocabulary that
+    ends inside a tile, whose logits would be 0, count nowhere."""
+    hidden, head, t, w = loss_inputs(n + v, n, v, d, dtype)
+    head[:, 0], hidden[:, 0] = 4.0, at / 4
+    got = run_loss(hidden, head, t, w)
+    assert all(torch.isfinite(x).all() for x in got) and float(got[1].min()) < at + 40
+    check_loss(hidden, head, t, w, 1.0, got)
+
+
+@pytest.mark.parametrize("n,v,d,dtype", [(8192, 17000, 64, BF), (4100, 11003, 64, FP)])
+def test_token_loss_logits_far_below_zero_in_pieces(n, v, d, dtype):
+    """The same with the gradient in two pieces of the vocabulary, the second ragged."""
+    hidden, head, t, w = loss_inputs(n + 1, n, v, d, dtype)
+    head[:, 0], hidden[:, 0] = 4.0, -30.0
+    got = run_loss(hidden, head, t, w)
+    assert all(torch.isfinite(x).all() for x in got)
+    check_loss(hidden, head, t, w, 1.0, got)
