@@ -21,11 +21,11 @@
 //
 // Accumulation: tcgen05 adds into fp32 accumulators with truncation, measured
 // here as a relative error of about 2e-6 at K = 2048 growing with K.  Where
-// the result is read in fp32 (the loss's logits; everything of fp32 operands)
-// the accumulator therefore covers `chunk` k-blocks only and the epilogue
-// threads add the chunks in registers, rounded to nearest.  What is rounded to
-// bf16 right away (P and the gradients of bf16 operands) takes one accumulator
-// over the whole contraction.
+// the result is read in fp32 (all logits, P's as the loss's; everything of fp32
+// operands) the accumulator therefore covers `chunk` k-blocks only and the
+// epilogue threads add the chunks in registers, rounded to nearest.  What is
+// rounded to bf16 right away (the gradients of bf16 operands) takes one
+// accumulator over the whole contraction.
 //
 // fp32 operands: x = hi + mid + lo with three bf16 terms (24 bits).  A k-block
 // is three stages, one for each term of both operands (lo first), and six
@@ -74,7 +74,7 @@ struct Smem {
 };
 
 constexpr int ROW_GROUP = 32;          // row tiles that share a vocabulary tile before the next one
-constexpr int LSE_CHUNK = 8;           // k-blocks per accumulator of the loss's logits (K = 512)
+constexpr int LSE_CHUNK = 8;           // k-blocks per accumulator of the logits of many rows (K = 512)
 constexpr int WHOLE_CHUNK = 1 << 16;   // ... of what is rounded to bf16 (K = 4 M: well inside the bounded waits)
 constexpr int F32_CHUNK = 1;           // ... of everything that fp32 operands give (six products of K = 64)
 constexpr float LOG2E = 1.4426950408889634f;
@@ -1629,12 +1629,20 @@ cudaError_t launch_f32_few(const LossParams& p, const void* hidden, const void* 
   return cudaGetLastError();
 }
 
-// k-blocks per accumulator of few rows' logits, K = 64 or 128: the truncation of
-// longer ones show: a row's loss is a small difference of two logits, and of
+// k-blocks per accumulator of the logits.  Few rows, K = 64 or 128: the truncation
+// of longer ones shows: a row's loss is a small difference of two logits, and of
 // one row nothing averages out (error of the loss of one row against 64 bits,
 // 12 inputs: K = 64 2.4e-7 in 98 us, K = 128 2.8e-7 in 94, K = 256 7.2e-7 in
 // 86; the plain fp32 form 2.0e-7).
-int few_chunk(int n, int planes) { return planes == 3 ? F32_CHUNK : (n <= 16 ? 1 : 2); }
+// The same for the loss and the gradient, whose P is made of exp(l - lse): with
+// the very logits that the lse is made of their errors cancel in 1 - p of a sure
+// target, with others (one accumulator over the whole width) they do not.  Rows
+// with 1 - p near 2e-4, error of their d_hidden: 4e-3 to 1e-2, against 0.44 (d =
+// 2048) and 2.1 (d = 8192), for 1 to 2 % of the gradient's time.
+int logit_chunk(int n, int planes) {
+  if (planes == 3) return F32_CHUNK;
+  return n <= 16 ? 1 : (n <= FEW_ROWS ? 2 : LSE_CHUNK);
+}
 
 // The head as the few-rows kernel reads it: boxes of 32 entries.
 cudaError_t few_head_map(CUtensorMap* map, const void* head, int v, int d, int pitch, int planes) {
@@ -1747,7 +1755,7 @@ static armt_status token_loss(armt_dtype dtype, int n, int vocab, int d, const v
     p.id_bytes = jp.id_bytes = target_bytes;
     p.block_err = (unsigned*)(ws + L.block_err);
     jp.block_err = p.block_err;
-    p.chunk = few_chunk(n, L.planes);
+    p.chunk = logit_chunk(n, L.planes);
     cudaError_t e;
     if (simt) {
       jp.blocks = 148;
@@ -1786,7 +1794,7 @@ static armt_status token_loss(armt_dtype dtype, int n, int vocab, int d, const v
     p.target = rp.target;
     jp.perm = rp.perm;
     p.tile_n = logit_tile(L.rows, vocab);   // the same for every pass: the parts are laid out for it
-    p.chunk = few ? few_chunk(n, L.planes) : (f32 ? F32_CHUNK : LSE_CHUNK);
+    p.chunk = logit_chunk(n, L.planes);
     if (few) e = nr <= 16 ? launch_few<LSE, 16>(maps, p, st) : launch_few<LSE, 64>(maps, p, st);
     else e = launch_products<LSE>(maps, p, (long long)div_up(nr, TILE) * div_up(vocab, p.tile_n), st);
     if (e == cudaSuccess) e = join(nr, r0);
@@ -1856,7 +1864,7 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     else if (few) e = load_map(&mg.a, ws + L.p, n, few_cols(n), p.vc, L.planes);
     else e = load_map(&mg.a, ws + L.p, 64, 64, n, p.panels * L.planes);
     if (e == cudaSuccess && !few) e = make_map(&mp.out0, ws + L.p, false, 64, 64, n, p.panels * L.planes, 64, 32);
-    p.chunk = f32 ? F32_CHUNK : WHOLE_CHUNK;
+    p.chunk = logit_chunk(n, L.planes);
     const int nt = div_up(p.vc, TILE);
     p.tile_n = logit_tile(n, p.vc);
     p.p_out = (bf16*)(ws + L.p);
@@ -1869,6 +1877,7 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     LossParams pg = p;
     pg.n_rows = L.g_rows;
     pg.two_terms = L.two_terms;
+    pg.chunk = f32 ? F32_CHUNK : WHOLE_CHUNK;
     const long long jobs = (p.want_dw ? (long long)nt * dt * L.dw_splits : 0) + (p.want_dh ? (long long)mt * dt * p.splits : 0);
     if (e == cudaSuccess) e = launch_products<GRAD>(mg, pg, jobs, st);
     if (e == cudaSuccess && d_head && L.dw_splits > 1) {

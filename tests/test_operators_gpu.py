@@ -806,3 +806,35 @@ def test_token_loss_logits_far_below_zero_in_pieces(n, v, d, dtype):
     got = run_loss(hidden, head, t, w)
     assert all(torch.isfinite(x).all() for x in got)
     check_loss(hidden, head, t, w, 1.0, got)
+
+
+# ------------------------------------------------------------------ P and lse from the same logits
+@pytest.mark.parametrize("n,v,d", [(1, 1000, 2048), (3, 1000, 8192), (40, 1000, 2048), (40, 1000, 8192), (200, 1000, 2048),
+                                   (200, 1000, 8192), (2000, 1000, 4096)])
+def test_token_loss_gradient_of_sure_rows(n, v, d):
+    """Targets of probability near 1 (1 - p about 2e-4, logits of 16, many columns): p - 1 is a
+    small difference.  Where P is made of the very logits that its lse is made of, their errors
+    el (as in logit_error) only change 1 - p by its el-th part; what is left is the rounding of
+    lse, of its sum and of the exponential."""
+    g = gen(n + d)
+    head = (randn(g, v, d) / math.sqrt(d)).to(BF)
+    t = torch.randint(0, v, (n,), generator=g, device="cuda")
+    hidden = (randn(g, n, d) + 16 * head[t].float()).to(BF)
+    w = torch.ones(n, device="cuda")
+    loss, lse, dh, dw = run_loss(hidden, head, t, w)
+    L, rl, _, A, _ = loss_reference(hidden, head, t, 1.0)
+    el = logit_error(A, d, 1) + L.abs().max(1).values * U
+    es = (16 + 64 + v / 256) * U + 4 * U * (rl.abs() + 1)      # as in check_loss: sum and logarithm
+    P = torch.exp(L - rl[:, None])
+    at = t[:, None]
+    Q = P.scatter_add(1, at, torch.full_like(P[:, :1], -1.0))
+    gap = (L - rl[:, None]).abs()
+    rest = -Q.gather(1, at)[:, 0]
+    assert float(rest.median()) < 1e-3
+    # the others: exp(l - lse) relative; the target: its complement
+    ep = P * (2 * el + es + 8 * U)[:, None] + P * gap * 3 * U
+    ep.scatter_(1, at, (rest * 2 * el + es + 8 * U)[:, None])
+    ep = ep + Q.abs() * (2.0 ** -16 if n <= 64 else half(BF))   # two terms of P, or one
+    W = head.double()
+    want = Q @ W
+    check(dh, want, ep @ W.abs() + Q.abs() @ W.abs() * ((v / 16 + 2) * 4 + 24) * U + want.abs() * half(BF) + 1e-38, "d_hidden")
