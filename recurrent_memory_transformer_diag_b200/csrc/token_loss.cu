@@ -22,10 +22,9 @@
 // Accumulation: tcgen05 adds into fp32 accumulators with truncation, measured
 // here as a relative error of about 2e-6 at K = 2048 growing with K.  Where
 // the result is read in fp32 (all logits, P's as the loss's; everything of fp32
-// operands) the accumulator therefore covers `chunk` k-blocks only and the
-// epilogue threads add the chunks in registers, rounded to nearest.  What is
-// rounded to bf16 right away (the gradients of bf16 operands) takes one
-// accumulator over the whole contraction.
+// operands) the accumulator therefore covers one to eight k-blocks only, where
+// it is rounded to bf16 right away (the gradients of bf16 operands) 128, and the
+// epilogue threads add these chunks in registers, rounded to nearest.
 //
 // fp32 operands: x = hi + mid + lo with three bf16 terms (24 bits).  A k-block
 // is three stages, one for each term of both operands (lo first), and six
@@ -75,7 +74,8 @@ struct Smem {
 
 constexpr int ROW_GROUP = 32;          // row tiles that share a vocabulary tile before the next one
 constexpr int LSE_CHUNK = 8;           // k-blocks per accumulator of the logits of many rows (K = 512)
-constexpr int WHOLE_CHUNK = 1 << 16;   // ... of what is rounded to bf16 (K = 4 M: well inside the bounded waits)
+constexpr int GRAD_CHUNK = 128;        // ... of the gradients of bf16 operands (K = 8192: 1e-5 where the type rounds by
+                                       // 2e-3; one over 262144 rows lost 3e-4.  K = 2048 took 1 to 2 % more time)
 constexpr int F32_CHUNK = 1;           // ... of everything that fp32 operands give (six products of K = 64)
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -1877,7 +1877,7 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
     LossParams pg = p;
     pg.n_rows = L.g_rows;
     pg.two_terms = L.two_terms;
-    pg.chunk = f32 ? F32_CHUNK : WHOLE_CHUNK;
+    pg.chunk = f32 ? F32_CHUNK : GRAD_CHUNK;
     const long long jobs = (p.want_dw ? (long long)nt * dt * L.dw_splits : 0) + (p.want_dh ? (long long)mt * dt * p.splits : 0);
     if (e == cudaSuccess) e = launch_products<GRAD>(mg, pg, jobs, st);
     if (e == cudaSuccess && d_head && L.dw_splits > 1) {

@@ -838,3 +838,28 @@ def test_token_loss_gradient_of_sure_rows(n, v, d):
     W = head.double()
     want = Q @ W
     check(dh, want, ep @ W.abs() + Q.abs() @ W.abs() * ((v / 16 + 2) * 4 + 24) * U + want.abs() * half(BF) + 1e-38, "d_hidden")
+
+
+def test_token_loss_head_gradient_of_many_rows():
+    """Sums over 262144 rows of one sign: no bias of a long accumulator.  Logits of 0 and 512
+    entries make P of every entry but the target exactly 2^-9, so that the only errors are those
+    of the sum: an accumulator of K = 8192 at most (512 instructions, 2 u in the instruction and
+    2 u in the accumulator), 32 of them added to nearest, the scale, and the last rounding (half
+    of the step where the result lies)."""
+    from recurrent_memory_transformer_diag_b200 import token_loss, token_loss_grad
+    n, v, d = 262144, 512, 8192
+    g = gen(71)
+    hidden = (1 + torch.rand(n, d, generator=g, device="cuda", dtype=BF)).mul_(
+        torch.linspace(1, 2, d, device="cuda").to(BF))
+    head = torch.zeros(v, d, dtype=BF, device="cuda")
+    t = torch.zeros(n, dtype=torch.int64, device="cuda")
+    loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    token_loss(hidden, head, t, loss, lse)
+    dw = torch.empty_like(head)
+    token_loss_grad(hidden, head, t, lse, torch.ones(n, device="cuda"), d_head=dw)
+    want = torch.zeros(d, dtype=torch.float64, device="cuda")
+    for part in hidden.split(8192):
+        want += part.double().sum(0)
+    want *= 2.0 ** -9
+    step = torch.exp2(torch.floor(torch.log2(want))) * 2.0 ** -7
+    check(dw[1:], want.expand(v - 1, d), (step / 2 + want * (512 * 4 + 32 + 2) * U).expand(v - 1, d))
