@@ -241,42 +241,53 @@ class Armt:
         return {L.armt_kernel_kind_name(k).decode(): (ms[k], cnt[k]) for k in range(n) if cnt[k]}
 
     def score(self, ids, targets, n_segments: int, seg_len: int, table, head, gain, loss, A, z,
-              embed_scale: float = 1.0, logit_scale: float = 1.0, carry_state: bool = False, stream=None):
+              embed_scale: float = 1.0, logit_scale: float = 1.0, carry_state: bool = False, stream=None,
+              workspace=None):
         """Per-token losses of a token sequence: embedding, forward, the norm in front
         of the head (gain; None leaves it out) and the vocabulary loss.
 
         ids, targets [n_segments * seg_len] (an id outside the table is padding, a
         target outside the vocabulary has loss 0); table, head [vocab, d] and gain [d]
         in the context's type; loss [n_segments * seg_len] fp32; A, z as in
-        ``forward_ex``.  The embeddings, hidden states and workspaces live for the
-        call, in PyTorch's allocator, on the call's stream."""
+        ``forward_ex``.  The embeddings and hidden states live for the call, in
+        PyTorch's allocator, on the call's stream, and so does the loss's workspace
+        unless the caller passes one (``workspace_bytes("token_loss", ...)`` bytes; its
+        ``workspace_status`` tells why losses are NaN).  What is refused, or finds no
+        memory, leaves A and z as they were."""
         from . import operators as ops
         w, c = "Armt.score", self.cfg
         n, d = n_segments * seg_len, c.d_model
-        # everything is looked at before the forward changes A and z
-        _, vocab, _, dev = ops._matrix(w, "table", table)
+        # everything is looked at, and allocated, before the forward changes A and z
+        kind, vocab, _, dev = ops._matrix(w, "table", table)
         dtype, f32 = ops.torch_type(c.dtype), ops.torch_type("fp32")
         ops._tensor(w, "table", table, dtype, (vocab, d), dev)
         ops._matrix(w, "head", head)
         ops._tensor(w, "head", head, dtype, (head.shape[0], d), dev)
         if gain is not None:
             ops._tensor(w, "gain", gain, dtype, (d,), dev)
+            ops._need("armt_rms_norm_grad_workspace", (kind, n, d))   # refuses sizes that the norm does not take
+            ops._aligned(w, "gain", gain)
+            ops._finite(w, "rms_eps", c.rms_eps)
         ops._ids(w, "ids", ids, n, dev)
         ops._ids(w, "targets", targets, n, dev)
         ops._tensor(w, "loss", loss, f32, (n,), dev)
         ops._tensor(w, "A", A, f32, (c.n_layers, d, c.phi_dim), dev)
         ops._tensor(w, "z", z, f32, (c.n_layers, c.phi_dim), dev)
-        ops._apart(w, [("loss", loss), ("A", A), ("z", z)],
-                   [("ids", ids), ("targets", targets), ("table", table), ("head", head), ("gain", gain)])
-        with ops.on_stream(stream, table.device):
-            x = table.new_empty(n, d)
+        ops._aligned(w, "table", table)
+        ops._aligned(w, "head", head)
+        ops._finite(w, "embed_scale", embed_scale)
+        ops._finite(w, "logit_scale", logit_scale)
+        inputs = [("ids", ids), ("targets", targets), ("table", table), ("head", head), ("gain", gain)]
+        ops._apart(w, [("loss", loss), ("A", A), ("z", z)], inputs + [("workspace", workspace)])
+        with ops.on_stream(stream, dev):
+            _, _, space = ops._space(w, "armt_token_loss_workspace", (kind, n, head.shape[0], d, 0), workspace, dev)
+            ops._apart(w, [("workspace", space)], inputs)
+            x, hidden, lse = table.new_empty(n, d), table.new_empty(n, d), loss.new_empty(n)
             ops.embed(ids, table, x, scale=embed_scale)
-            hidden = table.new_empty(n, d)
             self.forward_ex(x, n_segments, seg_len, hidden, A, z, carry_state)
             if gain is not None:
-                ops.rms_norm(hidden, gain, hidden, None, self.cfg.rms_eps)
-            lse = loss.new_empty(n)
-            ops.token_loss(hidden, head, targets, loss, lse, scale=logit_scale)
+                ops.rms_norm(hidden, gain, hidden, None, c.rms_eps)
+            ops.token_loss(hidden, head, targets, loss, lse, scale=logit_scale, workspace=space)
 
     def device_status(self, stream=None):
         _check(lib().armt_device_status(self._h, _stream_handle(stream)), "armt_device_status", self._h)

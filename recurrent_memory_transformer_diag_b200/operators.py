@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 from typing import Optional
 
 import torch
@@ -67,6 +68,17 @@ def _ids(where: str, name: str, t, n: Optional[int], device) -> int:
     if not t.is_contiguous() or t.dim() != 1 or (n is not None and t.shape[0] != n):
         _bad(where, f"{name} must be contiguous, one id per row")
     return size
+
+
+def _aligned(where: str, name: str, t):
+    """On a 16-byte boundary (the operators look at this themselves; for what they look at too late)."""
+    if t.data_ptr() % 16:
+        _bad(where, f"{name} must start on a 16-byte boundary")
+
+
+def _finite(where: str, name: str, x):
+    if not math.isfinite(ctypes.c_float(x).value):
+        _bad(where, f"{name} must be finite")
 
 
 def _apart(where: str, outputs, others):
@@ -131,6 +143,7 @@ def _space(where: str, size_fn: str, args, workspace, device):
             _bad(where, f"workspace is on {workspace.device}, not on {device}")
         if workspace.numel() < need:
             _bad(where, f"workspace holds {workspace.numel()} bytes, {need} are needed")
+        _aligned(where, "workspace", workspace)
     return workspace.data_ptr(), workspace.numel(), workspace
 
 

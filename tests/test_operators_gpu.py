@@ -863,3 +863,73 @@ def test_token_loss_head_gradient_of_many_rows():
     want *= 2.0 ** -9
     step = torch.exp2(torch.floor(torch.log2(want))) * 2.0 ** -7
     check(dw[1:], want.expand(v - 1, d), (step / 2 + want * (512 * 4 + 32 + 2) * U).expand(v - 1, d))
+
+
+# ------------------------------------------------------------------ Armt.score refuses before it changes the state
+def score_inputs(name="small", v=515):
+    from recurrent_memory_transformer_diag_b200 import CONFIGS
+    cfg = CONFIGS[name]
+    dt, n, d = BF if cfg.dtype == "bf16" else FP, 2 * cfg.seg_len, cfg.d_model
+    g = gen(41)
+    table, head = randn(g, v, d).to(dt), (randn(g, v, d) / math.sqrt(d)).to(dt)
+    ids = torch.randint(0, v, (n,), generator=g, device="cuda")
+    state = randn(g, cfg.n_layers, d, cfg.phi_dim) * 1e-2, torch.rand(cfg.n_layers, cfg.phi_dim, generator=g, device="cuda")
+    return cfg, dict(ids=ids, targets=ids.roll(-1), n_segments=2, seg_len=cfg.seg_len, table=table, head=head,
+                     gain=torch.ones(d, dtype=dt, device="cuda"), loss=torch.zeros(n, device="cuda"), A=state[0],
+                     z=state[1], carry_state=True)
+
+
+def off_by_one(x):
+    """The same numbers, dense, two or four bytes off a 16-byte boundary."""
+    y = torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")[1:].view(x.shape)
+    return y.copy_(x)
+
+
+@pytest.mark.parametrize("name", ["tiny", "small"])
+def test_score_refuses_before_the_state_changes(name, monkeypatch):
+    """What the norm and the loss would refuse after the forward, or could not allocate:
+    the streamed state and the losses stay, so that the segment can be scored again."""
+    from recurrent_memory_transformer_diag_b200 import Armt, ArmtError, make_weights, workspace_bytes, workspace_status
+    cfg, call = score_inputs(name)
+    n, d, v = len(call["ids"]), cfg.d_model, len(call["head"])
+    size = workspace_bytes("token_loss", call["head"].dtype, n, d, v)
+    space = torch.empty(size, dtype=torch.uint8, device="cuda")
+    head_size = call["head"].element_size()
+    shared = torch.zeros(size + v * d * head_size, dtype=torch.uint8, device="cuda")
+    with Armt(cfg, max_segments=2) as m:
+        m.load_weights(make_weights(cfg))
+        kept = [(k, call[k], call[k].clone()) for k in ("A", "z", "loss", "head", "table")]
+
+        def untouched():
+            torch.cuda.synchronize()
+            return all(torch.equal(a, b) for _, a, b in kept)
+        for wrong in (dict(head=off_by_one(call["head"])), dict(gain=off_by_one(call["gain"])),
+                      dict(table=off_by_one(call["table"])), dict(logit_scale=float("inf")),
+                      dict(logit_scale=float("nan")), dict(logit_scale=1e300), dict(embed_scale=float("nan")),
+                      dict(n_segments=3), dict(workspace=space[:-1]), dict(workspace=space.cpu()), dict(workspace=7),
+                      dict(workspace=shared, head=shared[:v * d * head_size].view(call["head"].dtype).view(v, d))):
+            with pytest.raises(ArmtError):
+                m.score(**{**call, **wrong})
+            assert untouched(), wrong.keys()
+        # no memory left for the loss
+        import recurrent_memory_transformer_diag_b200.operators as ops
+        real = torch.empty
+
+        def empty(*a, **k):
+            if k.get("dtype") is torch.uint8:
+                raise torch.cuda.OutOfMemoryError("no workspace")
+            return real(*a, **k)
+        monkeypatch.setattr(ops.torch, "empty", empty)
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            m.score(**call)
+        assert untouched()
+        monkeypatch.undo()
+        # the caller's own workspace: the same losses, and its status can be read
+        A, z = call["A"].clone(), call["z"].clone()
+        m.score(**call, workspace=space)
+        workspace_status(space)
+        want = call["loss"].clone()
+        assert float(want.min()) > 0 and not torch.equal(A, call["A"])
+        m.score(**{**call, "A": A, "z": z})
+        torch.cuda.synchronize()
+        assert torch.equal(call["loss"], want) and torch.equal(A, call["A"]) and torch.equal(z, call["z"])
