@@ -170,6 +170,8 @@ class Armt:
         h = ctypes.c_void_p()
         _check(lib().armt_create(ctypes.byref(self._c), ctypes.byref(h)), "armt_create")
         self._h = h
+        import torch
+        self.device_index = torch.cuda.current_device()   # where its weights and workspaces are
 
     # -- lifecycle
     def close(self):
@@ -259,6 +261,8 @@ class Armt:
         n, d = n_segments * seg_len, c.d_model
         # everything is looked at, and allocated, before the forward changes A and z
         kind, vocab, _, dev = ops._matrix(w, "table", table)
+        if dev.index != self.device_index:
+            ops._bad(w, f"table is on {dev}, the context on device {self.device_index}")
         dtype, f32 = ops.torch_type(c.dtype), ops.torch_type("fp32")
         ops._tensor(w, "table", table, dtype, (vocab, d), dev)
         ops._matrix(w, "head", head)

@@ -933,3 +933,19 @@ def test_score_refuses_before_the_state_changes(name, monkeypatch):
         m.score(**{**call, "A": A, "z": z})
         torch.cuda.synchronize()
         assert torch.equal(call["loss"], want) and torch.equal(A, call["A"]) and torch.equal(z, call["z"])
+
+
+def test_score_refuses_another_device_than_the_context_s(monkeypatch):
+    """A context's weights and workspaces are on one device; tensors of another are refused
+    (here by a context that takes itself for one of the next device)."""
+    from recurrent_memory_transformer_diag_b200 import Armt, ArmtError, make_weights
+    cfg, call = score_inputs("tiny")
+    with Armt(cfg, max_segments=2) as m:
+        m.load_weights(make_weights(cfg))
+        assert m.device_index == torch.cuda.current_device()
+        before = call["A"].clone()
+        monkeypatch.setattr(m, "device_index", m.device_index + 1)
+        with pytest.raises(ArmtError, match="device"):
+            m.score(**call)
+        torch.cuda.synchronize()
+        assert torch.equal(call["A"], before)
