@@ -284,8 +284,8 @@ class Armt:
         inputs = [("ids", ids), ("targets", targets), ("table", table), ("head", head), ("gain", gain)]
         ops._apart(w, [("loss", loss), ("A", A), ("z", z)], inputs + [("workspace", workspace)])
         with ops.on_stream(stream, dev):
-            _, _, space = ops._space(w, "armt_token_loss_workspace", (kind, n, head.shape[0], d, 0), workspace, dev)
-            ops._apart(w, [("workspace", space)], inputs)
+            _, _, space = ops._space(w, "armt_token_loss_workspace", (kind, n, head.shape[0], d, 0), workspace, dev,
+                                     inputs)
             x, hidden, lse = table.new_empty(n, d), table.new_empty(n, d), loss.new_empty(n)
             ops.embed(ids, table, x, scale=embed_scale)
             self.forward_ex(x, n_segments, seg_len, hidden, A, z, carry_state)

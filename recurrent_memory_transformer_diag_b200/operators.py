@@ -129,8 +129,9 @@ def _need(size_fn: str, args) -> int:
     return need.value
 
 
-def _space(where: str, size_fn: str, args, workspace, device):
-    """(address, bytes, tensor to keep until the launches are made)."""
+def _space(where: str, size_fn: str, args, workspace, device, inputs):
+    """(address, bytes, tensor to keep until the launches are made).  A given workspace
+    shares no memory with an input: it is written while the inputs are read."""
     need = _need(size_fn, args)
     if workspace is None:
         if need == 0:
@@ -144,6 +145,7 @@ def _space(where: str, size_fn: str, args, workspace, device):
         if workspace.numel() < need:
             _bad(where, f"workspace holds {workspace.numel()} bytes, {need} are needed")
         _aligned(where, "workspace", workspace)
+        _apart(where, [("workspace", workspace)], inputs)
     return workspace.data_ptr(), workspace.numel(), workspace
 
 
@@ -192,9 +194,10 @@ def embed_grad(ids, d_out, d_table, scale: float = 1.0, accumulate: bool = False
         _bad(w, "d_table must be a 2-d tensor")
     vocab = d_table.shape[0]
     _tensor(w, "d_table", d_table, d_out.dtype, (vocab, d), dev)
-    _apart(w, [("d_table", d_table)], [("d_out", d_out), ("ids", ids), ("workspace", workspace)])
+    inputs = [("d_out", d_out), ("ids", ids)]
+    _apart(w, [("d_table", d_table)], inputs + [("workspace", workspace)])
     with on_stream(stream, dev):
-        at, size, keep = _space(w, "armt_embed_grad_workspace", (t, n, vocab, d), workspace, dev)
+        at, size, keep = _space(w, "armt_embed_grad_workspace", (t, n, vocab, d), workspace, dev, inputs)
         _check(lib().armt_embed_grad(t, n, vocab, d, ids.data_ptr(), b, d_out.data_ptr(), scale, d_table.data_ptr(),
                                      int(bool(accumulate)), at, size, _handle(dev)), w)
 
@@ -229,7 +232,8 @@ def rms_norm_grad(x, gain, rstd, dy, dx, d_gain, workspace=None, stream=None):
     _apart(w, [("d_gain", d_gain)], [("x", x), ("gain", gain), ("rstd", rstd), ("dy", dy), ("dx", dx),
                                      ("workspace", workspace)])
     with on_stream(stream, dev):
-        at, size, keep = _space(w, "armt_rms_norm_grad_workspace", (t, n, d), workspace, dev)
+        at, size, keep = _space(w, "armt_rms_norm_grad_workspace", (t, n, d), workspace, dev,
+                                [("x", x), ("gain", gain), ("rstd", rstd), ("dy", dy)])
         _check(lib().armt_rms_norm_grad(t, n, d, x.data_ptr(), gain.data_ptr(), rstd.data_ptr(), dy.data_ptr(),
                                         dx.data_ptr(), d_gain.data_ptr(), at, size, _handle(dev)), w)
 
@@ -250,10 +254,10 @@ def token_loss(hidden, head, targets, loss, lse, scale: float = 1.0, workspace=N
     t, n, vocab, d, dev, b = _loss_args(w, hidden, head, targets)
     _tensor(w, "loss", loss, torch.float32, (n,), dev)
     _tensor(w, "lse", lse, torch.float32, (n,), dev)
-    _apart(w, [("loss", loss), ("lse", lse)], [("hidden", hidden), ("head", head), ("targets", targets),
-                                               ("workspace", workspace)])
+    inputs = [("hidden", hidden), ("head", head), ("targets", targets)]
+    _apart(w, [("loss", loss), ("lse", lse)], inputs + [("workspace", workspace)])
     with on_stream(stream, dev):
-        at, size, keep = _space(w, "armt_token_loss_workspace", (t, n, vocab, d, 0), workspace, dev)
+        at, size, keep = _space(w, "armt_token_loss_workspace", (t, n, vocab, d, 0), workspace, dev, inputs)
         _check(lib().armt_token_loss(t, n, vocab, d, hidden.data_ptr(), head.data_ptr(), targets.data_ptr(), b, scale,
                                      loss.data_ptr(), lse.data_ptr(), at, size, _handle(dev)), w)
 
@@ -275,10 +279,10 @@ def token_loss_grad(hidden, head, targets, lse, d_loss, d_hidden=None, d_head=No
         outs.append(("d_head", d_head))
     if not outs:
         _bad(w, "d_hidden or d_head must be given")
-    _apart(w, outs, [("hidden", hidden), ("head", head), ("targets", targets), ("lse", lse), ("d_loss", d_loss),
-                     ("workspace", workspace)])
+    inputs = [("hidden", hidden), ("head", head), ("targets", targets), ("lse", lse), ("d_loss", d_loss)]
+    _apart(w, outs, inputs + [("workspace", workspace)])
     with on_stream(stream, dev):
-        at, size, keep = _space(w, "armt_token_loss_workspace", (t, n, vocab, d, 1), workspace, dev)
+        at, size, keep = _space(w, "armt_token_loss_workspace", (t, n, vocab, d, 1), workspace, dev, inputs)
         _check(lib().armt_token_loss_grad(t, n, vocab, d, hidden.data_ptr(), head.data_ptr(), targets.data_ptr(), b,
                                           scale, lse.data_ptr(), d_loss.data_ptr(),
                                           None if d_hidden is None else d_hidden.data_ptr(),

@@ -949,3 +949,37 @@ def test_score_refuses_another_device_than_the_context_s(monkeypatch):
             m.score(**call)
         torch.cuda.synchronize()
         assert torch.equal(call["A"], before)
+
+
+@pytest.mark.parametrize("op,name", [("embed_grad", "d_out"), ("embed_grad", "ids"), ("rms_norm_grad", "x"),
+                                     ("rms_norm_grad", "gain"), ("rms_norm_grad", "rstd"), ("rms_norm_grad", "dy"),
+                                     ("token_loss", "hidden"), ("token_loss", "head"), ("token_loss", "targets"),
+                                     ("token_loss_grad", "hidden"), ("token_loss_grad", "head"),
+                                     ("token_loss_grad", "targets"), ("token_loss_grad", "lse"),
+                                     ("token_loss_grad", "d_loss")])
+def test_wrappers_refuse_inputs_inside_the_workspace(op, name):
+    """A workspace is written while the inputs are read: one input in it is refused, nothing is written."""
+    import recurrent_memory_transformer_diag_b200 as armt
+    n, v, d = 200, 300, 64
+    hidden, head, t, w = loss_inputs(1, n, v, d, BF)
+    t.clamp_(min=0)
+    new = lambda x: torch.zeros_like(x)  # noqa: E731
+    ins, outs = {
+        "embed_grad": (dict(ids=t, d_out=hidden), dict(d_table=new(head))),
+        "rms_norm_grad": (dict(x=hidden, gain=head[0].clone(), rstd=w, dy=hidden.clone()),
+                          dict(dx=new(hidden), d_gain=new(head[0]))),
+        "token_loss": (dict(hidden=hidden, head=head, targets=t), dict(loss=new(w), lse=new(w))),
+        "token_loss_grad": (dict(hidden=hidden, head=head, targets=t, lse=w, d_loss=w.clone()),
+                            dict(d_hidden=new(hidden), d_head=new(head))),
+    }[op]
+    size = armt.workspace_bytes(op, BF, n, d, v)
+    space = torch.zeros(size + ins[name].nbytes, dtype=torch.uint8, device="cuda")
+    at = (size // 2 + 255) // 256 * 256      # the input in the middle of what the operator would write
+    part = space[at:at + ins[name].nbytes].view(ins[name].dtype).view(ins[name].shape).copy_(ins[name])
+    before = space.clone()
+    with pytest.raises(armt.ArmtError, match="workspace overlaps"):
+        getattr(armt, op)(**{**ins, name: part}, **outs, workspace=space)
+    torch.cuda.synchronize()
+    assert torch.equal(space, before) and all((x == 0).all() for x in outs.values())
+    getattr(armt, op)(**ins, **outs, workspace=space)     # apart: fine
+    torch.cuda.synchronize()
