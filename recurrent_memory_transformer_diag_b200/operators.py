@@ -5,9 +5,12 @@ the norm in front of the head and the vocabulary loss, each with its gradients
 Each function checks its tensors (type, shape, dense layout, one device), hands
 their addresses to the C ABI on ``stream`` (default: PyTorch's current stream of
 the tensors' device) and returns without waiting; results go into the tensors
-that the caller passes.  A wrong argument raises ``ArmtError`` before anything
-is launched.  Workspaces come from PyTorch's allocator on the call's stream,
-unless the caller passes one (a uint8 tensor of ``workspace_bytes`` bytes).
+that the caller passes.  A wrong argument, or an empty one (no rows, no tokens),
+raises ``ArmtError`` before anything is launched.  Results carry no autograd
+history, but count as written in place: a backward pass that has kept one of
+those tensors raises instead of using the new values.  Workspaces come from
+PyTorch's allocator on the call's stream, unless the caller passes one (a uint8
+tensor of ``workspace_bytes`` bytes).
 """
 from __future__ import annotations
 
@@ -17,6 +20,7 @@ import math
 from typing import Optional
 
 import torch
+from torch.autograd.graph import increment_version as _written
 
 from .armt import ARMT_BF16, ARMT_FP32, ArmtError, _check, lib
 
@@ -182,6 +186,7 @@ def embed(ids, table, out, scale: float = 1.0, stream=None):
     with on_stream(stream, dev):
         _check(lib().armt_embed(t, n, vocab, d, ids.data_ptr(), b, table.data_ptr(), scale, out.data_ptr(),
                                 _handle(dev)), w)
+    _written(out)
 
 
 def embed_grad(ids, d_out, d_table, scale: float = 1.0, accumulate: bool = False, workspace=None, stream=None):
@@ -200,6 +205,7 @@ def embed_grad(ids, d_out, d_table, scale: float = 1.0, accumulate: bool = False
         at, size, keep = _space(w, "armt_embed_grad_workspace", (t, n, vocab, d), workspace, dev, inputs)
         _check(lib().armt_embed_grad(t, n, vocab, d, ids.data_ptr(), b, d_out.data_ptr(), scale, d_table.data_ptr(),
                                      int(bool(accumulate)), at, size, _handle(dev)), w)
+    _written(d_table)
 
 
 def rms_norm(x, gain, y, rstd=None, eps: float = 1e-5, stream=None):
@@ -216,6 +222,7 @@ def rms_norm(x, gain, y, rstd=None, eps: float = 1e-5, stream=None):
     with on_stream(stream, dev):
         _check(lib().armt_rms_norm(t, n, d, x.data_ptr(), gain.data_ptr(), eps, y.data_ptr(),
                                    None if rstd is None else rstd.data_ptr(), _handle(dev)), w)
+    _written(y if rstd is None else (y, rstd))
 
 
 def rms_norm_grad(x, gain, rstd, dy, dx, d_gain, workspace=None, stream=None):
@@ -236,6 +243,7 @@ def rms_norm_grad(x, gain, rstd, dy, dx, d_gain, workspace=None, stream=None):
                                 [("x", x), ("gain", gain), ("rstd", rstd), ("dy", dy)])
         _check(lib().armt_rms_norm_grad(t, n, d, x.data_ptr(), gain.data_ptr(), rstd.data_ptr(), dy.data_ptr(),
                                         dx.data_ptr(), d_gain.data_ptr(), at, size, _handle(dev)), w)
+    _written((dx, d_gain))
 
 
 def _loss_args(w, hidden, head, targets):
@@ -260,6 +268,7 @@ def token_loss(hidden, head, targets, loss, lse, scale: float = 1.0, workspace=N
         at, size, keep = _space(w, "armt_token_loss_workspace", (t, n, vocab, d, 0), workspace, dev, inputs)
         _check(lib().armt_token_loss(t, n, vocab, d, hidden.data_ptr(), head.data_ptr(), targets.data_ptr(), b, scale,
                                      loss.data_ptr(), lse.data_ptr(), at, size, _handle(dev)), w)
+    _written((loss, lse))
 
 
 def token_loss_grad(hidden, head, targets, lse, d_loss, d_hidden=None, d_head=None, scale: float = 1.0,
@@ -287,3 +296,4 @@ def token_loss_grad(hidden, head, targets, lse, d_loss, d_hidden=None, d_head=No
                                           scale, lse.data_ptr(), d_loss.data_ptr(),
                                           None if d_hidden is None else d_hidden.data_ptr(),
                                           None if d_head is None else d_head.data_ptr(), at, size, _handle(dev)), w)
+    _written([x for _, x in outs])

@@ -983,3 +983,31 @@ def test_wrappers_refuse_inputs_inside_the_workspace(op, name):
     assert torch.equal(space, before) and all((x == 0).all() for x in outs.values())
     getattr(armt, op)(**ins, **outs, workspace=space)     # apart: fine
     torch.cuda.synchronize()
+
+
+def test_results_count_as_written_in_place():
+    """Autograd notices that a tensor it has kept was overwritten by an operator (as by any
+    in-place operation), and inputs do not count as written."""
+    from recurrent_memory_transformer_diag_b200 import (embed, embed_grad, rms_norm, rms_norm_grad, token_loss,
+                                                        token_loss_grad)
+    n, v, d = 12, 40, 64
+    hidden, head, t, w = loss_inputs(70, n, v, d, FP)
+    gain, f = torch.ones(d, device="cuda"), lambda: torch.empty(n, device="cuda")
+    out = lambda x: torch.empty_like(x)  # noqa: E731
+    calls = [(embed, (t, head), (out(hidden),)), (embed_grad, (t, hidden), (out(head),)),
+             (rms_norm, (hidden, gain), (out(hidden), f())),
+             (rms_norm_grad, (hidden, gain, w, hidden), (out(hidden), out(gain))),
+             (token_loss, (hidden, head, t), (f(), f())),
+             (token_loss_grad, (hidden, head, t, w, w), (out(hidden), out(head)))]
+    for fn, ins, outs in calls:
+        before = [x._version for x in ins + outs]
+        fn(*ins, *outs)
+        after = [x._version for x in ins + outs]
+        k = len(ins)
+        assert after[:k] == before[:k] and all(a > b for a, b in zip(after[k:], before[k:])), fn.__name__
+    x = torch.ones(n, d, device="cuda")
+    p = torch.ones(n, d, device="cuda", requires_grad=True)
+    y = (p * x).sum()          # keeps x
+    rms_norm(x, gain, x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
