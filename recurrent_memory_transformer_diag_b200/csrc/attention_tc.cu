@@ -38,6 +38,7 @@
 // All mbarrier waits are bounded; on timeout the kernel sets the error word,
 // drains its copies and MMAs, frees TMEM and exits.
 #include "armt_internal.cuh"
+#include "copies_in_flight.cuh"
 #include "tcgen05_ptx.cuh"
 
 namespace armt {
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // Q tiles (two buffers per warpgroup) are loaded when a head is about to
       // start at the latest, and one head ahead whenever the buffer is free.
       bool ok = true;
-      uint32_t armed = 0;   // bits 0-3: Q buffers, 4-6: K stages, 8-9: V stages with loads in flight
+      CopiesInFlight copies;   // stages 0-3: Q buffers, 4-7: K, 8-10: V
       int qi_a = 0, qi_b = 0;            // Q loads issued per warpgroup
       int qr_a = 0, qk_a = 0;   // item round and head of warpgroup A's next Q load
       int qr_b = 0, qk_b = 0;
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (issuer)
             tma_load_3d(&tm_qk, &q_full[qb], smem + OFF_Q + qb * Q_BYTES + h * HALF_BYTES,
                         (g * grp + w + 2 * qk) * HD + h * 64, q0, nd.z);
-        armed |= 1u << qb;
+        copies.issued(qb, qi / QB);
         ++qi;
         if (++qk >= (w ? heads_b : heads_a)) { qk = 0; ++qr; }
         return 1;
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int vt_outer = nd.z * p.KV + g;
         if (issuer) tma_load_3d(&tm_vt, &v_full[vs], vt, j * BKEY, 0, vt_outer);
         if (issuer) tma_load_3d(&tm_vt, &v_full[vs], vt + VT_BLK, j * BKEY + 64, 0, vt_outer);
-        armed |= 256u << vs;
+        copies.issued(8 + vs, kidx / V_STAGES);
         return true;
       };
       if (blockIdx.x < n_items) {
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               if (issuer)
                 tma_load_3d(&tm_qk, &k_full[ks], smem + OFF_K + ks * K_BYTES + h * HALF_BYTES, (p.H + g) * HD + h * 64,
                             j * BKEY, nd.z);
-            armed |= 16u << ks;
+            copies.issued(4 + ks, kidx / K_STAGES);
           }
           if (has_prev && !load_v(prev)) { ok = false; break; }
           // one head ahead, if that buffer is already free
@@ -379,18 +380,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (issuer) atomicOr(p.err, 16u);
         *abort_flag = 1;
       }
-      if (*abort_flag) {   // let every issued copy land before the CTA exits
-        const unsigned long long t0 = global_ns();
-        for (int b = 0; b < 2 * QB; ++b)
-          if (armed & (1u << b))
-            while (!mbar_try_wait(&q_full[b], 0) && !mbar_try_wait(&q_full[b], 1) && global_ns() - t0 < WAIT_LIMIT_NS) {}
-        for (int b = 0; b < K_STAGES; ++b)
-          if (armed & (16u << b))
-            while (!mbar_try_wait(&k_full[b], 0) && !mbar_try_wait(&k_full[b], 1) && global_ns() - t0 < WAIT_LIMIT_NS) {}
-        for (int b = 0; b < V_STAGES; ++b)
-          if (armed & (256u << b))
-            while (!mbar_try_wait(&v_full[b], 0) && !mbar_try_wait(&v_full[b], 1) && global_ns() - t0 < WAIT_LIMIT_NS) {}
-      }
+      // every issued copy lands before the CTA ends
+      const unsigned long long t0 = global_ns();
+      copies.drain([&](int s, uint32_t par) {
+                     return mbar_try_wait(s < 4 ? &q_full[s] : (s < 8 ? &k_full[s - 4] : &v_full[s - 8]), par);
+                   },
+                   [&] { return global_ns() - t0 > WAIT_LIMIT_NS; });
     }
   } else if (warp == 1 || warp == 2) {
     // ---------------- MMA issuers: warp 1 for warpgroup A, warp 2 for B ----------------

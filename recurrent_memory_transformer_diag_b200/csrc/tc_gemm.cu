@@ -53,6 +53,7 @@
 
 #include "armt_internal.cuh"
 #include "tc_gemm.cuh"
+#include "copies_in_flight.cuh"
 #include "tcgen05_ptx.cuh"
 
 namespace armt {
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const bool issuer = elect_one();
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t armed = 0;   // bit s: stage s has an issued load not yet seen complete by the consumer
+      CopiesInFlight copies;
       bool ok = true;
       for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
         const int node = t / tiles_per_node, r = t - node * tiles_per_node;
@@ -507,14 +508,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const bool swapped = SM::SWAP && p.swap_tail && mb == p.m_tiles - 1;
         for (int kb = 0; kb < p.k_blocks; ++kb) {
           if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
-          armed &= ~(1u << stage);
           uint8_t* sa = smem + stage * SM::STAGE_BYTES;
           if (!p.debug_no_loads) {
             if (issuer) mbar_expect_tx(&full[stage], swapped ? SM::SWAP_A_BYTES + SM::B_BYTES : SM::STAGE_BYTES);
             if (issuer)
               tma_load_3d(swapped ? &tmAs : &tmA, &full[stage], sa, kb * BKE, p.row0 + mb * BM, a_outer);
             if (issuer) tma_load_3d(&tmB, &full[stage], sa + SM::A_BYTES, kb * BKE, nb * BN, nd.y);
-            armed |= 1u << stage;
+            copies.issued(stage, phase);
           }
           if (++stage == SM::STAGES) { stage = 0; phase ^= 1; }
         }
@@ -523,17 +523,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (issuer) atomicOr(p.err, 1u);
         *abort_flag = 1;
       }
-      // drain: wait (bounded) until every issued copy has landed
-      if (*abort_flag) {
-        for (int s = 0; s < SM::STAGES; ++s) {
-          if (!(armed & (1u << s))) continue;
-          const unsigned long long t0 = global_ns();
-          // the latest phase of stage s is either complete or will complete; poll both parities
-          while (!mbar_try_wait(&full[s], 0) && !mbar_try_wait(&full[s], 1)) {
-            if (global_ns() - t0 > WAIT_LIMIT_NS) break;
-          }
-        }
-      }
+      // wait (bounded) until every issued copy has landed
+      const unsigned long long t0 = global_ns();
+      copies.drain([&](int s, uint32_t par) { return mbar_try_wait(&full[s], par); },
+                   [&] { return global_ns() - t0 > WAIT_LIMIT_NS; });
     }
   } else if (warp == 1) {
     {
@@ -778,7 +771,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const bool issuer = elect_one();
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t armed = 0;
+      CopiesInFlight copies;
       bool ok = true;
       const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);   // the even CTA's full[0]
       for (int t = cid; t < total && ok; t += ncl) {
@@ -790,13 +783,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         const int brow = nb * 256 + (int)rank * 128;
         for (int kb = 0; kb < p.k_blocks; ++kb) {
           if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
-          armed &= ~(1u << stage);
           uint8_t* sa = smem + stage * SM::STAGE_BYTES;
           if (leader && issuer) mbar_expect_tx(&full[stage], 2 * SM::STAGE_BYTES);   // both CTAs' copies
           const uint32_t fb = full0 + (uint32_t)(stage * sizeof(uint64_t));
           if (issuer) tma_load_3d_pair(&tmA, fb, sa, kb * BK, arow, a_outer);
           if (issuer) tma_load_3d_pair(&tmB, fb, sa + SM::A_BYTES, kb * BK, brow, nd.y);
-          armed |= 1u << stage;
+          copies.issued(stage, phase);
           if (++stage == SM::STAGES) { stage = 0; phase ^= 1; }
         }
       }
@@ -804,14 +796,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (issuer) atomicOr(p.err, 1u);
         *abort_flag = 1;
       }
-      if (*abort_flag && leader) {   // copies of both CTAs are counted on the even CTA's barriers
-        for (int s = 0; s < SM::STAGES; ++s) {
-          if (!(armed & (1u << s))) continue;
-          const unsigned long long t0 = global_ns();
-          while (!mbar_try_wait_cluster(&full[s], 0) && !mbar_try_wait_cluster(&full[s], 1)) {
-            if (global_ns() - t0 > WAIT_LIMIT_NS) break;
-          }
-        }
+      if (leader) {   // copies of both CTAs are counted on the even CTA's barriers
+        const unsigned long long t0 = global_ns();
+        copies.drain([&](int s, uint32_t par) { return mbar_try_wait_cluster(&full[s], par); },
+                     [&] { return global_ns() - t0 > WAIT_LIMIT_NS; });
       }
     }
   } else if (warp == 1) {

@@ -39,6 +39,7 @@
 #include <mutex>
 
 #include "armt_internal.cuh"
+#include "copies_in_flight.cuh"
 #include "tcgen05_ptx.cuh"
 #include "vec8.cuh"
 
@@ -522,7 +523,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     // ---------------- copies (both CTAs; whole warp, one elected lane issues) ----------------
     const bool issuer = elect_one();
     int stage = 0;
-    uint32_t phase = 0, armed = 0;
+    uint32_t phase = 0;
+    CopiesInFlight copies;
     bool ok = true;
     const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
     for (int t = cid; t < jobs.total && ok; t += ncl) {
@@ -533,7 +535,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const int am = j.m0 + (int)rank * 128, bn = j.n0 + (int)rank * (j.n / 2);
       for (int kb = 0, q = p.planes - 1; kb < j.kblocks;) {   // q: the term of both operands
         if (!wait_warp<true>(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
-        armed &= ~(1u << stage);
         uint8_t* sa = smem + stage * STAGE_BYTES;
         if (issuer && !p.debug_no_loads) {
           // both CTAs' copies
@@ -552,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                                q);
           }
         }
-        armed |= 1u << stage;
+        if (!p.debug_no_loads) copies.issued(stage, phase);
         if (++stage == STAGES) { stage = 0; phase ^= 1; }
         if (--q < 0) { q = p.planes - 1; ++kb; }
       }
@@ -561,14 +562,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       if (issuer) atomicOr(p.err, 1u);
       *abort_flag = 1;
     }
-    if (*abort_flag && leader) {   // copies of both CTAs are counted on the even CTA's barriers
-      for (int s = 0; s < STAGES; ++s) {
-        if (!(armed & (1u << s))) continue;
-        const unsigned long long t0 = global_ns();
-        while (!mbar_try_wait_cluster(&full[s], 0) && !mbar_try_wait_cluster(&full[s], 1)) {
-          if (global_ns() - t0 > WAIT_LIMIT_NS) break;
-        }
-      }
+    if (leader) {   // copies of both CTAs are counted on the even CTA's barriers
+      const unsigned long long t0 = global_ns();
+      copies.drain([&](int s, uint32_t par) { return mbar_try_wait_cluster(&full[s], par); },
+                   [&] { return global_ns() - t0 > WAIT_LIMIT_NS; });
     }
   } else if (warp == 1) {
     if (leader) {
@@ -817,13 +814,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   if (warp == 0) {
     const bool issuer = elect_one();
     int stage = 0;
-    uint32_t phase = 0, armed = 0;
+    uint32_t phase = 0;
+    CopiesInFlight copies;
     bool ok = true;
     for (int t = v0; t < v1 && ok; t += 128) {
       const int v = p.v0 + t, boxes = (min(v1 - t, 128) + 31) / 32;
       for (int kb = 0, q = p.planes - 1; kb < kblocks;) {
         if (!wait_warp<false>(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
-        armed &= ~(1u << stage);
         uint8_t* sa = smem + stage * SM::STAGE;
         if (issuer && !p.debug_no_loads) {
           mbar_expect_tx(&full[stage], boxes * (BOX_BYTES / 2) + SM::H_BYTES);
@@ -831,7 +828,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             tma_load_3d(&maps.b, &full[stage], sa + h * (BOX_BYTES / 2), kb * BK, v + 32 * h, q);
           tma_load_3d(&maps.a, &full[stage], sa + 2 * BOX_BYTES, kb * BK, 0, q);
         }
-        armed |= 1u << stage;
+        if (!p.debug_no_loads) copies.issued(stage, phase);
         if (++stage == SM::N_STAGES) { stage = 0; phase ^= 1; }
         if (--q < 0) { q = p.planes - 1; ++kb; }
       }
@@ -840,14 +837,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       if (issuer) atomicOr(err, 1u);
       *abort_flag = 1;
     }
-    if (*abort_flag) {   // every issued copy lands before the CTA ends
-      for (int s = 0; s < SM::N_STAGES; ++s) {
-        if (!(armed & (1u << s))) continue;
-        const unsigned long long t0 = global_ns();
-        while (!mbar_try_wait(&full[s], 0) && !mbar_try_wait(&full[s], 1)) {
-          if (global_ns() - t0 > WAIT_LIMIT_NS) break;
-        }
-      }
+    {   // every issued copy lands before the CTA ends
+      const unsigned long long t0 = global_ns();
+      copies.drain([&](int s, uint32_t par) { return mbar_try_wait(&full[s], par); },
+                   [&] { return global_ns() - t0 > WAIT_LIMIT_NS; });
     }
   } else if (warp == 1) {
     const bool issuer = elect_one();
