@@ -26,6 +26,23 @@ struct CopiesInFlight {
     parity = (parity & ~(1u << s)) | (phase_parity & 1u) << s;
   }
 
+  // Those of these copies that `other`, the pair's other CTA, has not issued.
+  ARMT_COPIES_FN CopiesInFlight beyond(const CopiesInFlight& other) const {
+    CopiesInFlight r;
+    r.stages = stages & ~(other.stages & ~(parity ^ other.parity));
+    r.parity = parity;
+    return r;
+  }
+
+  // In one word, for at most 16 stages.
+  ARMT_COPIES_FN uint32_t word() const { return (stages & 0xffffu) | parity << 16; }
+  ARMT_COPIES_FN static CopiesInFlight of(uint32_t word) {
+    CopiesInFlight r;
+    r.stages = word & 0xffffu;
+    r.parity = word >> 16;
+    return r;
+  }
+
   // landed(s, parity): whether that phase of stage s is complete; late(): whether
   // the limit is over.  True once every copy has landed.
   template <class Landed, class Late>

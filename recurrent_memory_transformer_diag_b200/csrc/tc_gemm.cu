@@ -727,6 +727,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* skip_word = tmem_slot + 2;
+  uint32_t* sent = tmem_slot + 3;   // [rank]: the stages each CTA has issued copies to, in both CTAs
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -745,6 +746,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     // an earlier kernel of this forward already gave up on a wait: the pair
     // skips its work (the even CTA decides for both)
     *skip_word = *reinterpret_cast<volatile unsigned*>(p.err) & ERR_WAIT_TIMEOUT_MASK;
+    sent[0] = sent[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -795,6 +797,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       if (!ok) {
         if (issuer) atomicOr(p.err, 1u);
         *abort_flag = 1;
+      }
+      if (issuer) {
+        st_cluster_u32(mapa_shared(smem_u32(&sent[rank]), 0), copies.word());
+        st_cluster_u32(mapa_shared(smem_u32(&sent[rank]), 1), copies.word());
       }
       if (leader) {   // copies of both CTAs are counted on the even CTA's barriers
         const unsigned long long t0 = global_ns();
@@ -881,6 +887,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   tc_fence_before();
   cluster_sync_all();   // no MMA, copy or epilogue of either CTA still uses TMEM or shared memory
   tc_fence_after();
+  if (sent[0] != sent[1]) {
+    // a wait ran out: the odd CTA may have issued copies to stages that the even
+    // one has not armed (where the even one is ahead, the odd one's have landed).
+    // Those are armed for it here, and waited for
+    if (leader && warp == 0) {
+      const CopiesInFlight rest = CopiesInFlight::of(sent[1]).beyond(CopiesInFlight::of(sent[0]));
+      auto landed = [&](int s, uint32_t par) { return mbar_try_wait_cluster(&full[s], par); };
+      if (lane < SM::STAGES && (rest.stages >> lane & 1u) && !landed(lane, rest.parity >> lane & 1u))
+        mbar_expect_tx(&full[lane], SM::STAGE_BYTES);
+      __syncwarp();
+      const unsigned long long t0 = global_ns();
+      rest.drain(landed, [&] { return global_ns() - t0 > WAIT_LIMIT_NS; });
+    }
+    cluster_sync_all();
+  }
   if (warp == 1) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
   }

@@ -479,6 +479,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* skip_word = tmem_slot + 2;
+  uint32_t* sent = tmem_slot + 3;      // [rank]: the stages each CTA has issued copies to, in both CTAs
+  uint32_t* narrow = tmem_slot + 5;    // of the odd CTA's, in the even one: those of 128 columns (three boxes, not four)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -497,6 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     // an earlier kernel of this call already gave up on a wait: skip the work
     // (the even CTA decides for both)
     *skip_word = *reinterpret_cast<volatile unsigned*>(p.err) & ERR_WAIT_TIMEOUT_MASK;
+    sent[0] = sent[1] = *narrow = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -523,7 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     // ---------------- copies (both CTAs; whole warp, one elected lane issues) ----------------
     const bool issuer = elect_one();
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, of_128 = 0;
     CopiesInFlight copies;
     bool ok = true;
     const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
@@ -554,6 +557,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           }
         }
         if (!p.debug_no_loads) copies.issued(stage, phase);
+        of_128 = (of_128 & ~(1u << stage)) | (j.n == 128 ? 1u << stage : 0u);
         if (++stage == STAGES) { stage = 0; phase ^= 1; }
         if (--q < 0) { q = p.planes - 1; ++kb; }
       }
@@ -561,6 +565,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     if (!ok) {
       if (issuer) atomicOr(p.err, 1u);
       *abort_flag = 1;
+    }
+    if (issuer) {
+      st_cluster_u32(mapa_shared(smem_u32(&sent[rank]), 0), copies.word());
+      st_cluster_u32(mapa_shared(smem_u32(&sent[rank]), 1), copies.word());
+      if (!leader) st_cluster_u32(mapa_shared(smem_u32(narrow), 0), of_128);
     }
     if (leader) {   // copies of both CTAs are counted on the even CTA's barriers
       const unsigned long long t0 = global_ns();
@@ -691,6 +700,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   tc_fence_before();
   cluster_sync_all();   // no product, copy or epilogue of either CTA still uses TMEM or shared memory
   tc_fence_after();
+  if (sent[0] != sent[1]) {
+    // a wait ran out: the odd CTA may have issued copies to stages that the even
+    // one has not armed (where the even one is ahead, the odd one's have landed).
+    // Those are armed for it here, and waited for (by an epilogue warp: the
+    // control warps have given their registers away)
+    if (leader && warp == 4) {
+      const CopiesInFlight rest = CopiesInFlight::of(sent[1]).beyond(CopiesInFlight::of(sent[0]));
+      auto landed = [&](int s, uint32_t par) { return mbar_try_wait_cluster(&full[s], par); };
+      if (lane < STAGES && (rest.stages >> lane & 1u) && !landed(lane, rest.parity >> lane & 1u))
+        mbar_expect_tx(&full[lane], (*narrow >> lane & 1u ? 3 : 4) * BOX_BYTES);
+      __syncwarp();
+      const unsigned long long t0 = global_ns();
+      rest.drain(landed, [&] { return global_ns() - t0 > WAIT_LIMIT_NS; });
+    }
+    cluster_sync_all();
+  }
   if (warp == 1) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
   }

@@ -71,13 +71,106 @@ int main() {
 """
 
 
-@pytest.fixture(scope="module")
-def model(tmp_path_factory):
+# A CTA pair: the copies of both are counted, in bytes, on the even CTA's barriers, which
+# the even CTA arms for both; the CTAs stop at different stages.
+PAIR = r"""
+#include "copies_in_flight.cuh"
+#include <cstdio>
+#include <random>
+#include <vector>
+
+struct Bar {
+  int phase = 0, arrived = 0, tx = 0;
+  bool twice = false;   // armed again before the phase was complete
+  void check() { if (arrived && tx == 0) { ++phase; arrived = 0; } }
+  void expect(int bytes) { twice |= arrived != 0; tx += bytes; arrived = 1; check(); }
+  void land(int bytes) { tx -= bytes; check(); }
+  bool done(unsigned parity) const { return ((phase & 1) != 0) != (parity != 0); }
+};
+struct Copy { int cta, stage, bytes, at; };
+
+int main() {
+  std::mt19937 rng(11);
+  long odd_alone = 0, even_alone = 0, armed_late = 0;
+  for (int trial = 0; trial < 20000; ++trial) {
+    const int stages = 1 + rng() % 7, total = rng() % 40;
+    std::vector<Bar> bar(stages);
+    std::vector<Copy> flying;
+    armt::CopiesInFlight mine[2];
+    std::vector<int> bytes(stages);
+    int now = 0, sent[2] = {0, 0}, used = 0;
+    const int stop[2] = {(int)(rng() % 100), (int)(rng() % 100)};
+    auto tick = [&] {
+      ++now;
+      for (size_t i = 0; i < flying.size();) {
+        if (flying[i].at <= now) {
+          bar[flying[i].stage].land(flying[i].bytes);
+          flying.erase(flying.begin() + i);
+        } else {
+          ++i;
+        }
+      }
+    };
+    for (; now < 100; tick()) {
+      for (int c = 0; c < 2; ++c) {
+        if (now >= stop[c] || sent[c] >= total || sent[c] - used >= stages || rng() % 3 == 0) continue;
+        const int s = sent[c] % stages, size = 3 + sent[c] * 7 % 2;   // of three or four boxes
+        if (c == 0) bar[s].expect(2 * size);
+        else bytes[s] = size;
+        flying.push_back({c, s, size, now + 1 + (int)(rng() % 9)});
+        mine[c].issued(s, sent[c] / stages & 1);
+        ++sent[c];
+      }
+      if (used < sent[0] && used < sent[1] && bar[used % stages].done(used / stages & 1)) ++used;
+    }
+    odd_alone += sent[1] > sent[0];
+    even_alone += sent[0] > sent[1];
+    auto landed = [&](int s, uint32_t par) { return bar[s].done(par); };
+    int t0 = now;
+    const bool all = mine[0].drain(landed, [&] { tick(); return now - t0 > 50; });
+    if (all != (sent[1] >= sent[0])) { printf("even drain %d\n", all); return 1; }
+    if (mine[0].word() != mine[1].word()) {
+      const auto rest = armt::CopiesInFlight::of(mine[1].word()).beyond(armt::CopiesInFlight::of(mine[0].word()));
+      for (int s = 0; s < stages; ++s)
+        if ((rest.stages >> s & 1) && !landed(s, rest.parity >> s & 1)) { bar[s].expect(bytes[s]); ++armed_late; }
+      t0 = now;
+      if (!rest.drain(landed, [&] { tick(); return now - t0 > 50; })) { printf("rest does not land\n"); return 1; }
+    }
+    for (auto& b : bar)
+      if (b.twice) { printf("armed twice\\n"); return 1; }
+    if (!flying.empty()) { printf("%zu copies in flight\n", flying.size()); return 1; }
+  }
+  printf("%ld %ld %ld\n", odd_alone, even_alone, armed_late);
+  return 0;
+}
+"""
+
+
+def run(tmp_path_factory, text):
     d = tmp_path_factory.mktemp("copies")
     src, exe = d / "model.cpp", d / "model"
-    src.write_text(HARNESS)
+    src.write_text(text)
     subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", CSRC, str(src), "-o", str(exe)], check=True)
     return subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+
+
+@pytest.fixture(scope="module")
+def model(tmp_path_factory):
+    return run(tmp_path_factory, HARNESS)
+
+
+def test_pair_waits_for_copies_of_stages_that_only_the_odd_cta_used(tmp_path_factory):
+    r = run(tmp_path_factory, PAIR)
+    assert r.returncode == 0, r.stdout
+    odd_alone, even_alone, armed_late = map(int, r.stdout.split())
+    assert odd_alone > 1000 and even_alone > 1000 and armed_late > 1000
+
+
+@pytest.mark.parametrize("name", ["tc_gemm.cu", "token_loss.cu"])
+def test_pair_kernels_exchange_the_record(name):
+    text = open(os.path.join(CSRC, name)).read()
+    assert text.count("copies.word()") == 2 and text.count("rest.drain(") == 1
+    assert text.index("copies.word()") < text.index("copies.drain(", text.index("copies.word()")) < text.index("rest.drain(")
 
 
 def test_drain_waits_for_every_copy(model):
