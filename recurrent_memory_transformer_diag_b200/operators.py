@@ -115,7 +115,8 @@ def on_stream(stream, device):
     if stream is None:
         return _HERE if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+        # 0 is the default stream; PyTorch would take it for "any stream of the pool"
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
     if stream.device != device:
         _bad("stream", f"the stream belongs to {stream.device}, the tensors to {device}")
     return torch.cuda.stream(stream)

@@ -1011,3 +1011,37 @@ def test_results_count_as_written_in_place():
     rms_norm(x, gain, x)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+def test_raw_handle_of_the_default_stream():
+    """Handle 0 is the default stream (what current_stream().cuda_stream gives there): a call on it
+    comes after what is queued there and before what follows."""
+    from recurrent_memory_transformer_diag_b200 import rms_norm
+    assert torch.cuda.current_stream().cuda_stream == 0
+    x = torch.zeros(256, 64, device="cuda")
+    gain, y, z = torch.ones(64, device="cuda"), torch.empty_like(x), torch.empty_like(x)
+    rms_norm(x, gain, y)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        x.zero_()
+        torch.cuda._sleep(20_000_000)      # some 10 ms
+        x.fill_(2.0)
+        rms_norm(x, gain, y, None, 0.0, stream=torch.cuda.current_stream().cuda_stream)
+        z.copy_(y)
+        y.zero_()
+        torch.cuda.synchronize()
+        assert (z == 1).all() and (y == 0).all()
+
+
+@pytest.mark.parametrize("n", [40, 300, 3000])
+def test_loss_on_the_default_stream_s_handle(n):
+    hidden, head, t, w = loss_inputs(80, n, 3000, 64, BF)
+    want = run_loss(hidden, head, t, w)
+    from recurrent_memory_transformer_diag_b200 import token_loss, token_loss_grad
+    for _ in range(10):
+        loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        dh, dw = torch.empty_like(hidden), torch.empty_like(head)
+        token_loss(hidden, head, t, loss, lse, stream=0)
+        token_loss_grad(hidden, head, t, lse, w, dh, dw, stream=0)
+        got = loss.clone(), lse.clone(), dh.clone(), dw.clone()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
