@@ -347,7 +347,8 @@ armt_status armt_memory_write_static(int M, int d, int d_key, int nu, float eps,
  * dtype is ARMT_FP32 or ARMT_BF16, one type for all tensors marked [type];
  * sums, norms and softmax statistics are fp32 in both.  Tensors are dense and
  * row-major, d a multiple of 8 (at most 2^20; n and vocab at most 2^30), their
- * base addresses on 16-byte boundaries; outputs and workspaces overlap nothing
+ * base addresses on 16-byte boundaries (d_gain and what is not [type]: on
+ * multiples of their elements' size); outputs and workspaces overlap nothing
  * else but where it says so.
  * ids / targets are int32 (id_bytes 4) or int64 (8).  All pointers are device
  * pointers of the current device.  Everything is asynchronous on `stream`,

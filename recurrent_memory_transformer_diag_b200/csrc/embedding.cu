@@ -633,7 +633,7 @@ extern "C" armt_status armt_embed(armt_dtype dtype, int n, int vocab, int d, con
   const armt_status s = check_sizes(dtype, n, vocab, d);
   if (s != ARMT_OK) return s;
   if (!ids || !table || !out || (id_bytes != 4 && id_bytes != 8) || !std::isfinite(scale) || !aligned16(table) ||
-      !aligned16(out))
+      !aligned16(out) || !aligned_to(ids, id_bytes))
     return ARMT_ERR_INVALID_ARG;
   const int vecs = d / 8;
   const long long total = (long long)n * vecs;
@@ -665,7 +665,8 @@ extern "C" armt_status armt_embed_grad(armt_dtype dtype, int n, int vocab, int d
   const armt_status s = armt_embed_grad_workspace(dtype, n, vocab, d, &need);
   if (s != ARMT_OK) return s;
   if (!ids || !d_out || !d_table || (id_bytes != 4 && id_bytes != 8) || !std::isfinite(scale) ||
-      (accumulate != 0 && accumulate != 1) || !aligned16(d_out) || !aligned16(d_table) || workspace_bytes < need ||
+      (accumulate != 0 && accumulate != 1) || !aligned16(d_out) || !aligned16(d_table) ||
+      !aligned_to(ids, id_bytes) || workspace_bytes < need ||
       (need && (!workspace || !aligned16(workspace))))
     return ARMT_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;

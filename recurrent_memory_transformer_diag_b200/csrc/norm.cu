@@ -267,7 +267,8 @@ extern "C" armt_status armt_rms_norm(armt_dtype dtype, int n, int d, const void*
                                      void* y, float* rstd, void* stream) {
   const armt_status s = check_norm(dtype, n, d);
   if (s != ARMT_OK) return s;
-  if (!x || !gain || !y || !(eps >= 0.f) || !std::isfinite(eps) || !aligned16(x) || !aligned16(gain) || !aligned16(y))
+  if (!x || !gain || !y || !(eps >= 0.f) || !std::isfinite(eps) || !aligned16(x) || !aligned16(gain) ||
+      !aligned16(y) || !aligned_to(rstd, 4))
     return ARMT_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == ARMT_BF16) return cuda_status(norm<bf16>((const bf16*)x, (const bf16*)gain, (bf16*)y, rstd, n, d, eps, st));
@@ -290,7 +291,8 @@ extern "C" armt_status armt_rms_norm_grad(armt_dtype dtype, int n, int d, const 
   const armt_status s = armt_rms_norm_grad_workspace(dtype, n, d, &need);
   if (s != ARMT_OK) return s;
   if (!x || !gain || !rstd || !dy || !dx || !d_gain || !workspace || workspace_bytes < need || !aligned16(x) ||
-      !aligned16(gain) || !aligned16(dy) || !aligned16(dx) || !aligned16(workspace))
+      !aligned16(gain) || !aligned16(dy) || !aligned16(dx) || !aligned16(workspace) || !aligned_to(rstd, 4) ||
+      !aligned_to(d_gain, dtype == ARMT_BF16 ? 2 : 4))
     return ARMT_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == ARMT_BF16)

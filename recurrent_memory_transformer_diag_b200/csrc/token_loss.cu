@@ -1741,7 +1741,8 @@ static armt_status token_loss(armt_dtype dtype, int n, int vocab, int d, const v
   armt_status s = check_sizes(dtype, n, vocab, d);
   if (s != ARMT_OK) return s;
   if (!hidden || !head || !targets || !loss || !lse || !workspace || !std::isfinite(scale) ||
-      (target_bytes != 4 && target_bytes != 8) || !aligned16(hidden) || !aligned16(head) || !aligned16(workspace))
+      (target_bytes != 4 && target_bytes != 8) || !aligned16(hidden) || !aligned16(head) || !aligned16(workspace) ||
+      !aligned_to(targets, target_bytes) || !aligned_to(loss, 4) || !aligned_to(lse, 4))
     return ARMT_ERR_INVALID_ARG;
   const bool f32 = dtype == ARMT_FP32;
   const Layout L(n, vocab, d, f32, false);
@@ -1835,7 +1836,8 @@ extern "C" armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, 
   if (s != ARMT_OK) return s;
   if (!hidden || !head || !targets || !lse || !d_loss || (!d_hidden && !d_head) || !workspace ||
       !std::isfinite(scale) || (target_bytes != 4 && target_bytes != 8) || !aligned16(hidden) || !aligned16(head) ||
-      !aligned16(workspace) || !aligned16(d_hidden) || !aligned16(d_head))
+      !aligned16(workspace) || !aligned16(d_hidden) || !aligned16(d_head) || !aligned_to(targets, target_bytes) ||
+      !aligned_to(lse, 4) || !aligned_to(d_loss, 4))
     return ARMT_ERR_INVALID_ARG;
   const bool f32 = dtype == ARMT_FP32;
   const Layout L(n, vocab, d, f32, true);

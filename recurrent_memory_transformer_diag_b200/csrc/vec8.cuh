@@ -61,6 +61,8 @@ __device__ __forceinline__ long long load_id(const void* p, int bytes, long long
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// On a multiple of its elements' size (ids; single numbers a row).
+inline bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 // Sizes and types that the operators at the ends of the model share.
 inline armt_status check_sizes(armt_dtype dtype, int n, int v, int d) {

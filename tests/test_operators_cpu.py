@@ -114,3 +114,18 @@ def test_workspace_bytes(libarmt):
 def test_exports_are_bound(libarmt):
     for name in ("armt_embed", "armt_rms_norm", "armt_token_loss", "armt_token_loss_grad", "armt_workspace_status"):
         assert name in armt.EXPORTS and getattr(libarmt, name).argtypes
+
+
+@pytest.mark.parametrize("name,base,change", [
+    (f, b, c) for f, b, changes in [
+        ("armt_embed", EMBED, [dict(ids=A + 4), dict(ids=A + 2, id_bytes=4)]),
+        ("armt_embed_grad", EMBED_GRAD, [dict(ids=A + 4), dict(ids=A + 1, id_bytes=4)]),
+        ("armt_rms_norm", NORM, [dict(rstd=A + 2)]),
+        ("armt_rms_norm_grad", NORM_GRAD, [dict(rstd=A + 2), dict(d_gain=A + 1), dict(d_gain=A + 2, dtype=0)]),
+        ("armt_token_loss", LOSS, [dict(targets=A + 4), dict(targets=A + 3, target_bytes=4), dict(loss=A + 2),
+                                   dict(lse=A + 1)]),
+        ("armt_token_loss_grad", LOSS_GRAD, [dict(targets=A + 4), dict(lse=A + 2), dict(d_loss=A + 3)]),
+    ] for c in changes])
+def test_refusals_of_numbers_off_their_own_size(libarmt, name, base, change):
+    """ids, targets and single numbers a row need no 16-byte boundary, but their own size."""
+    assert getattr(libarmt, name)(*{**base, **change}.values()) == INVALID
