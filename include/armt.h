@@ -392,7 +392,8 @@ armt_status armt_rms_norm_grad(armt_dtype dtype, int n, int d, const void* x, co
  * lse[i] - l[i, targets[i]] ([n] fp32).  Rows whose target is outside
  * [0, vocab) are skipped: loss and lse are 0 there, whatever the row holds.
  * The logits are never kept: the workspace holds two numbers per row and 128
- * vocabulary entries for 8192 rows at a time.
+ * vocabulary entries for 8192 rows at a time, these rows once more, and for fp32
+ * rows (more than 16 of them) the head as three bf16 terms, 6 vocab d bytes.
  * _workspace: grad 0 for armt_token_loss, 1 for armt_token_loss_grad. */
 armt_status armt_token_loss_workspace(armt_dtype dtype, int n, int vocab, int d, int grad, size_t* bytes);
 armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d, const void* hidden, const void* head,
@@ -403,9 +404,13 @@ armt_status armt_token_loss(armt_dtype dtype, int n, int vocab, int d, const voi
  * ([type]; either may be null), from the lse of armt_token_loss with the same
  * inputs.  The logits are computed again, one piece of the vocabulary at a
  * time; softmax minus one-hot, divided by the largest finite |d_loss|, enters the
- * products as bf16 (as three bf16 terms, 24 bits, for fp32).  Rows without a
- * target have a zero gradient and add nothing to the head's, whatever they
- * hold (d_loss and lse of such rows are not read). */
+ * products as bf16 (as two bf16 terms up to 64 rows; as three, 24 bits, for
+ * fp32).  The workspace holds that of one piece (256 MB, or 256 columns where
+ * they take more), partial sums of d_hidden in fp32 (one for each of its
+ * elements with many rows, up to 256 with few; for few tiles of d_head of that
+ * too), the rows once more, and for fp32 the head as three bf16 terms.  Rows
+ * without a target have a zero gradient and add nothing to the head's, whatever
+ * they hold (d_loss and lse of such rows are not read). */
 armt_status armt_token_loss_grad(armt_dtype dtype, int n, int vocab, int d, const void* hidden, const void* head,
                                  const void* targets, int target_bytes, float scale, const float* lse,
                                  const float* d_loss, void* d_hidden, void* d_head, void* workspace,

@@ -194,7 +194,9 @@ __global__ void __launch_bounds__(256) sort_count_kernel(const void* ids, int id
 }
 
 // Moves the block's keys to their places, in order.  Each block adds up the
-// counts before it by itself (blocks x RADIX counts, from L2).
+// counts before it by itself (blocks x RADIX counts, from L2: 8 MB in all for
+// 131072 tokens, but with the square of them: 134 GB, tens of milliseconds a
+// pass, for 16 million).
 __global__ void __launch_bounds__(256) sort_move_kernel(const void* ids, int id_bytes, const int* keys, const int* pos,
                                                         int n, int vocab, int shift, const int* hist, int* out_keys,
                                                         int* out_pos) {

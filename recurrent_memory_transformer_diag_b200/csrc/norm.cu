@@ -86,7 +86,9 @@ __global__ void __launch_bounds__(32 * NORM_WARPS) rms_norm_kernel(const T* x, c
 // 8 up to 4096 columns) leave room for many blocks, which hide each other's
 // latencies; more warps to a row would spend more instructions on the row's
 // sums than on its elements.  At 32771 x 2048: one warp to a row 104 us, eight
-// 117, four 73 (5.5 TB/s).
+// 117, four 73 (5.5 TB/s).  Wider rows take four groups a lane and spill 144 to
+// 212 bytes a thread; with 2^26 elements, gain included: bf16 81 us up to 4096
+// columns, 95 at 8192, 98 at 16384 (4.2 TB/s); fp32 131, 158, 190.
 template <typename T, int VPL, int W>
 struct NormGrad {
   static constexpr int WARPS_PER_SM = VPL * sizeof(T) <= 4 ? 24 : 16;

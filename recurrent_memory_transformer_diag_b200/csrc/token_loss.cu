@@ -9,11 +9,19 @@
 // One tensor-core kernel computes every product, in three roles:
 //   LSE   logits tile by tile; each tile leaves (max, sum of exponentials) of
 //         its columns per row and the target's logit, joined by a small kernel
-//   PROB  logits of one vocabulary piece again, turned into P (bf16)
+//   PROB  logits of one vocabulary piece again, turned into P (bf16: half a step
+//         of bf16 a value, as an operand of the products.  Up to 64 rows, where
+//         few roundings average out, two terms; fp32 operands three.  Errors of
+//         the gradients of bf16 operands against 64 bits: 1.9e-3 to 2.3e-3, of
+//         which the results' own rounding is 1.7e-3; a second term for all rows would
+//         double the products of both gradients)
 //   GRAD  both gradients of the piece from P in one launch: dW tiles contract
 //         over the rows, dH tiles over the piece's columns
-// A piece of the vocabulary is as wide as P of that piece stays within a fixed
-// budget, so the memory is independent of the vocabulary.
+// A piece of the vocabulary is as wide as P of that piece stays within 256 MB (of
+// 256 columns at least: more from 524288 bf16 rows on), so no logits or P of the
+// whole vocabulary are kept.  What does grow with it: fp32 operands' head as
+// three bf16 terms (6 bytes an element) and, of the loss, two numbers per row
+// and 128 entries for 8192 rows at a time.
 //
 // Rows are put in order first: rows with a target in front, the others behind
 // them as zeros (so what stands in a masked row cannot reach the head's
@@ -752,7 +760,10 @@ __device__ __forceinline__ int target_of(const void* ids, int id_bytes, int i, i
 // of head per SM in the pair kernel), and the products cost next to nothing.
 // Thread = vocabulary entry; LSE keeps a running (max, sum) per hidden row in
 // registers over all tiles of the CTA and joins the 32 lanes at the end.  One
-// row against 131072 x 2048: 98 us, 5.5 TB/s.
+// row against 131072 x 2048: 98 us, 5.5 TB/s.  The loss against 50021 x 2048, in
+// whole calls: 1 row 53 us, 16 rows 55 (66 and 68 with 64 columns), 17 to 64
+// rows 60; the pair kernel takes 67 for 17 rows and the same 60 from 64 on (fp32
+// operands, 17 rows: 312 here, 419 there).
 
 // Entries per block of the few-rows kernel: one block per SM of the B200, in
 // steps of 32 (tiles of 128 dealt round leave half of the SMs idle in the last
@@ -1038,16 +1049,20 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 
 // ---------------------------------------------------------------------------
 // LSE and PROB of up to 16 fp32 rows: bound by reading the fp32 head once, which
-// splitting it into bf16 terms would not allow (13 rows, 43440 x 1704: 292 us
-// that way).  Plain fp32 multiply-adds: the hidden rows in shared memory, a
-// warp four vocabulary entries at a time so that every value read from there
-// meets four head values; the 4 x NT sums are spread over the lanes while they
-// are added up across the warp, and each lane keeps (max, sum) of one row.  The
-// gradient's logits come from here too: they have to be the very numbers that
-// the lse was made of, or the difference (1e-6 of a logit of 14) shows in P.
+// splitting it into bf16 terms would not allow.  Plain fp32 multiply-adds: the
+// hidden rows in shared memory, a warp four vocabulary entries at a time so that
+// every value read from there meets four head values; the 4 x NT sums are spread
+// over the lanes while they are added up across the warp, and each lane keeps
+// (max, sum) of one row.  The gradient's logits come from here too: they have to
+// be the very numbers that the lse was made of, or the difference (1e-6 of a
+// logit of 14) shows in P.
+// The loss against 50021 x 2048 (410 MB: 64 us), in whole calls: 1 to 4 rows 104
+// to 106 us, 5 to 16 rows 180 to 187 (shared memory: each head value meets NT
+// rows); four rows through the form of 16 177, 1 to 16 rows through the three
+// terms 297 to 300.
 constexpr int F32_FEW_ROWS = 16;
 constexpr int F32_FEW_SMEM = 200 * 1024;
-constexpr int F32_FEW_THREADS = 384;   // 168 registers: the sums stay in them
+constexpr int F32_FEW_THREADS = 384;   // 168 registers: all but 56 to 84 bytes of 16 rows' sums stay in them
 
 // Sum over the lanes of N values each; lane l ends with values l, l + 32, ...
 // (N a multiple of 32) in v[0 .. N/32-1].
@@ -1486,7 +1501,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const JoinRows p) {
 
 constexpr int COUNTED_FROM = 2048;                 // rows from which they are counted first (8192 rows: 19 + 4 us, 37 without)
 constexpr int LOSS_ROWS = 8192;                    // rows per forward pass: bounds the (max, sum) workspace
-constexpr long long P_BYTES = 256ll << 20;         // P of one vocabulary piece
+constexpr long long P_BYTES = 256ll << 20;         // P of one vocabulary piece, where 256 columns fit
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 int round_up(int a, int b) { return (a + b - 1) / b * b; }
