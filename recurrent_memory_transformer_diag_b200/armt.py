@@ -171,7 +171,8 @@ class Armt:
         _check(lib().armt_create(ctypes.byref(self._c), ctypes.byref(h)), "armt_create")
         self._h = h
         import torch
-        self.device_index = torch.cuda.current_device()   # where its weights and workspaces are
+        # where its weights and workspaces are (None: PyTorch has no CUDA, and no tensors there)
+        self.device_index = torch.cuda.current_device() if torch.cuda.is_available() else None
 
     # -- lifecycle
     def close(self):

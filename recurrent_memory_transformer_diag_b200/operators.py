@@ -150,7 +150,7 @@ def _space(where: str, size_fn: str, args, workspace, device, inputs):
         if workspace.numel() < need:
             _bad(where, f"workspace holds {workspace.numel()} bytes, {need} are needed")
         _aligned(where, "workspace", workspace)
-        _apart(where, [("workspace", workspace)], inputs)
+        _apart(where, [("workspace", workspace.view(-1)[:need])], inputs)   # what is used of it
     return workspace.data_ptr(), workspace.numel(), workspace
 
 

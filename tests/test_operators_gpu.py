@@ -1045,3 +1045,16 @@ def test_loss_on_the_default_stream_s_handle(n):
         token_loss_grad(hidden, head, t, lse, w, dh, dw, stream=0)
         got = loss.clone(), lse.clone(), dh.clone(), dw.clone()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_inputs_behind_what_is_used_of_a_workspace():
+    """One arena for all: inputs behind the bytes that the operator asks for are no overlap."""
+    from recurrent_memory_transformer_diag_b200 import token_loss, workspace_bytes
+    n, v, d = 100, 300, 64
+    hidden, head, t, w = loss_inputs(90, n, v, d, BF)
+    size = (workspace_bytes("token_loss", BF, n, d, v) + 255) // 256 * 256
+    arena = torch.zeros(size + hidden.nbytes, dtype=torch.uint8, device="cuda")
+    inside = arena[size:].view(BF).view(n, d).copy_(hidden)
+    loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    token_loss(inside, head, t, loss, lse, workspace=arena)
+    assert torch.equal(inside, hidden) and torch.equal(loss, run_loss(hidden, head, t, w)[0])
