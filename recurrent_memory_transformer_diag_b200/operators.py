@@ -172,6 +172,8 @@ def workspace_bytes(op: str, dtype: torch.dtype, n: int, d: int, vocab: int = 1)
 def workspace_status(workspace, stream=None):
     """Wait for the stream; raises if a bounded wait ran out in the last
     ``token_loss`` or ``token_loss_grad`` call that used this workspace."""
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or workspace.nbytes < 4:
+        _bad("armt_workspace_status", "workspace must be a tensor on a CUDA device")
     with on_stream(stream, workspace.device):
         _check(lib().armt_workspace_status(workspace.data_ptr(), _handle(workspace.device)), "armt_workspace_status")
 

@@ -129,3 +129,10 @@ def test_exports_are_bound(libarmt):
 def test_refusals_of_numbers_off_their_own_size(libarmt, name, base, change):
     """ids, targets and single numbers a row need no 16-byte boundary, but their own size."""
     assert getattr(libarmt, name)(*{**base, **change}.values()) == INVALID
+
+
+@pytest.mark.parametrize("workspace", [None, 5, torch.zeros(64, dtype=torch.uint8)])
+def test_status_of_what_is_no_workspace(workspace):
+    with pytest.raises(ArmtError, match="CUDA device") as e:
+        ops.workspace_status(workspace)
+    assert e.value.status == INVALID
