@@ -1058,3 +1058,25 @@ def test_inputs_behind_what_is_used_of_a_workspace():
     loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
     token_loss(inside, head, t, loss, lse, workspace=arena)
     assert torch.equal(inside, hidden) and torch.equal(loss, run_loss(hidden, head, t, w)[0])
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n", [3, 40, 200])
+def test_token_loss_entries_masked_by_the_lowest_value(n, dtype):
+    """Vocabulary entries whose logit is the type's lowest number (whole tiles among them) have no
+    part in the loss and no gradient: the same as without them, to the order of the sums."""
+    v, d = 900, 64
+    hidden, head, t, w = loss_inputs(95, n, v, d, dtype, ignored=0.0)
+    masked = torch.rand(v, generator=gen(96), device="cuda") < 0.5
+    masked[256:640] = True
+    masked[t] = False
+    hidden[:, 0], head[:, 0] = 1.0, 0.0
+    head[masked, 0] = torch.finfo(dtype).min
+    got = run_loss(hidden, head, t, w)
+    keep = (~masked).nonzero()[:, 0]
+    place = torch.zeros(v, dtype=torch.int64, device="cuda")
+    place[keep] = torch.arange(len(keep), device="cuda")
+    few = head[keep].contiguous()
+    want = run_loss(hidden, few, place[t], w)
+    check_loss(hidden, few, place[t], w, 1.0, (*got[:3], got[3][keep].contiguous()))
+    assert (got[3][masked] == 0).all() and float((got[0] - want[0]).abs().max()) < 64 * U * float(want[1].abs().max() + 1)
